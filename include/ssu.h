@@ -4,8 +4,10 @@
  * The Mamba selective state update over a paged recurrent-state pool, in its forms
  * (single-token decode, multi-token prefill with an optional replay stash, tree verify
  * of a draft tree, and the replay of accepted speculative tokens or tree nodes), plus
- * slot clear, slot copy and gather/scatter; and the gated delta-rule decode core over a
- * pool with the same conventions.
+ * slot clear, slot copy and gather/scatter; the causal convolution before it, over single
+ * tokens, prompts and trees; the selective scan with a decay per channel and state; the
+ * verification of drafted tokens; and the gated delta-rule decode core over a pool with
+ * the same conventions.
  *
  * Sources: the "Selective State Update" page of the TensorRT-Edge-LLM C++ API
  * (mamba_ssm::invokeSelectiveStateUpdate, invokeSelectiveStateUpdatePrefill,
@@ -80,7 +82,7 @@ typedef enum {
                                  queried before it) */
     SSU_ERR_ALIGN = 6         /* pool pointer or slot stride not 16-byte aligned, or (in
                                  ssu_prefill / ssu_replay / ssu_ddtree) B, C or the stash B
-                                 not 16-byte aligned */
+                                 not 16-byte aligned, or (scan_*) A not 16-byte aligned */
 } ssu_status;
 
 enum {
@@ -95,8 +97,12 @@ enum {
     SSU_FLAG_TREE = 64,           /* ssu_ddtree: a node's parent walk was malformed (its
                                      outputs are 0); replay: an accepted node id outside
                                      [0, T) (the row was left untouched) */
-    SSU_FLAG_DUPLICATE_INDEX = 128 /* ssu_check_state_indices only: two active rows name
+    SSU_FLAG_DUPLICATE_INDEX = 128, /* ssu_check_state_indices only: two active rows name
                                      the same slot */
+    SSU_FLAG_TOKEN = 256,         /* spec_verify: a drafted token outside [0, vocab): it is
+                                     not accepted */
+    SSU_FLAG_NO_MASS = 512        /* spec_verify: the row to draw the next token from holds
+                                     no positive finite probability: the token is -1 */
 };
 
 /* Per-layer device pointers of a multi-layer replay: one entry per layer, in a device
@@ -242,6 +248,148 @@ int ssu_conv_decode(const void *xbc, int x_dtype, const void *conv_weight,
                     int32_t P, void *out, const int32_t *state_indices, int32_t batch,
                     int32_t active_batch, int32_t nheads, int32_t ngroups, int32_t dim,
                     int32_t dstate, int dt_softplus, int32_t *err_flags, ssu_stream_t stream);
+
+/*
+ * ssu_conv_prefill -- the causal conv1d of ssu_conv_decode over T tokens of raw xBC channels,
+ * from the slot's window, as separate tensors for ssu_prefill, ssu_ddtree or scan_prefill.
+ * For t < L_b = context_lengths[b] (all T when NULL) and every channel c, with in[t] the raw
+ * input of token t and in[-1], in[-2], ... the window from its newest tap backwards:
+ *     v[t,c] = conv_bias[c] + sum_k conv_weight[c,k] * in[t - (width-1) + k, c],
+ *     times sigmoid(v[t,c]) if conv_silu
+ * computed in fp32 and rounded once into x (channels [0, x_dim)), B and C (the next two
+ * blocks of bc_dim).
+ *   xbc          [batch, T, x_dim + 2*bc_dim] x_dtype, consecutive tokens (and rows)
+ *                xbc_stride elements apart: a slice of wider rows is taken in place
+ *   conv_weight  [x_dim + 2*bc_dim, width] x_dtype;  conv_bias (optional) x_dtype
+ *   conv_state   conv pool as in ssu_conv_decode (channel-major, tap-major or any strides
+ *                that keep a slot's taps apart); unused when width == 1
+ *   x            [batch, T, x_dim] x_dtype;  B, C [batch, T, bc_dim] x_dtype (NULL when
+ *                bc_dim == 0); positions t >= L_b are not written
+ *   update_state != 0: the window becomes the last width-1 of (window, the row's L_b
+ *                tokens); 0: the pool is only read (verification: the accepted tokens enter
+ *                by ssu_conv_replay)
+ *   tree_parent_ids [batch, T] int32 (optional, as in ssu_ddtree; needs update_state == 0):
+ *                the inputs before node t are its ancestors (parent, grandparent, ...), then
+ *                the window. A node with a parent outside [-1, L_b) among its width-1
+ *                nearest ancestors gets outputs 0 and SSU_FLAG_TREE.
+ *   width 1..16. Padding rows write zeros to the outputs at every t < T.
+ * xbc must not overlap the outputs. One launch.
+ */
+int ssu_conv_prefill(const void *xbc, int x_dtype, int64_t xbc_stride, const void *conv_weight,
+                     const void *conv_bias, void *conv_state, int64_t conv_slot_stride,
+                     int64_t conv_stride_c, int64_t conv_stride_k, int32_t width, int conv_silu,
+                     int32_t P, void *x, void *B, void *C, const int32_t *state_indices,
+                     const int32_t *context_lengths, const int32_t *tree_parent_ids,
+                     int update_state, int32_t batch, int32_t active_batch, int32_t T,
+                     int32_t x_dim, int32_t bc_dim, int32_t *err_flags, ssu_stream_t stream);
+
+/*
+ * ssu_conv_replay -- commit accepted speculative tokens to the conv windows: the companion of
+ * ssu_replay for the convolution state. For k_b = accepted_lengths[b], the window of every
+ * channel becomes the last width-1 of (window, the raw inputs of the row's first k_b tokens);
+ * with accepted_node_ids [batch, max_accept_len] the t-th of them is xbc[b, ids[b][t]].
+ *   xbc [batch, T, conv_dim] x_dtype as given to ssu_conv_prefill; other arguments as there.
+ * Lengths and ids follow ssu_replay: k_b is bounded by T (by max_accept_len with ids), a row
+ * with an id outside [0, T) among its first k_b is left untouched and flagged SSU_FLAG_TREE.
+ * The taps are copied, bit for bit. One launch.
+ */
+int ssu_conv_replay(const void *xbc, int x_dtype, int64_t xbc_stride, void *conv_state,
+                    int64_t conv_slot_stride, int64_t conv_stride_c, int64_t conv_stride_k,
+                    int32_t width, int32_t P, const int32_t *accepted_lengths,
+                    const int32_t *state_indices, int32_t batch, int32_t active_batch, int32_t T,
+                    int32_t conv_dim, const int32_t *accepted_node_ids, int32_t max_accept_len,
+                    int32_t *err_flags, ssu_stream_t stream);
+
+/*
+ * scan_prefill -- the selective scan with a step for every channel and a decay for every
+ * (channel, state), over T tokens in one launch. For t < L_b = context_lengths[b], channel d
+ * of group g = d / (channels / ngroups) and state n:
+ *     s      = softplus(dt[t,d] + dt_bias[d]) if dt_softplus, else dt[t,d] + dt_bias[d]
+ *     h[d,n] = exp(s * A[d,n]) * h[d,n] + s * x[t,d] * B[t,g,n]
+ *     out    = sum_n h[d,n] * C[t,g,n] + D[d] * x[t,d],  times silu(z[t,d]) if z is given
+ * with h held in fp32 on chip across the tokens.
+ *   x, z     [batch, T, channels] x_dtype;  dt [batch, T, channels] dt_dtype
+ *   A        [channels, dstate] fp32, 16-byte aligned;  dt_bias, D [channels] fp32 (optional)
+ *   B, C     [batch, T, ngroups, dstate] bc_dtype
+ *   x_stride, dt_stride, z_stride, B_stride, C_stride: elements between consecutive tokens
+ *            (and rows) of each, so that slices of wider rows are taken in place
+ *   state    pool [P, channels, dstate] state_dtype, slot stride slot_stride elements
+ *   out      [batch, T, channels] x_dtype dense; t >= L_b is not written; NULL advances the
+ *            state only (C, D and z are then not read)
+ *   update_state != 0: the state after L_b tokens is stored once (not when L_b == 0);
+ *            0: the pool is only read (needs out)
+ * A speculative draft is verified with update_state = 0 and committed by a second call with
+ * out = NULL and the accepted lengths as context_lengths. Padding rows write zeros to out at
+ * every t < T. dstate in {8, 16, 32, 64, 128, 256}.
+ */
+int scan_prefill(const void *x, int x_dtype, int64_t x_stride, const void *dt, int dt_dtype,
+                 int64_t dt_stride, const float *A, const void *B, const void *C, int bc_dtype,
+                 int64_t B_stride, int64_t C_stride, const float *dt_bias, const float *D,
+                 const void *z, int64_t z_stride, void *state, int state_dtype,
+                 int64_t slot_stride, int32_t P, void *out, const int32_t *state_indices,
+                 const int32_t *context_lengths, int update_state, int32_t batch,
+                 int32_t active_batch, int32_t T, int32_t channels, int32_t ngroups,
+                 int32_t dstate, int dt_softplus, int32_t *err_flags, ssu_stream_t stream);
+
+/*
+ * scan_decode -- one token of scan_prefill's recurrence for every active row, the state
+ * updated in place. x, z, out [batch, channels], dt [batch, channels], B, C
+ * [batch, ngroups, dstate], the strides between rows; other arguments as in scan_prefill.
+ */
+int scan_decode(const void *x, int x_dtype, int64_t x_stride, const void *dt, int dt_dtype,
+                int64_t dt_stride, const float *A, const void *B, const void *C, int bc_dtype,
+                int64_t B_stride, int64_t C_stride, const float *dt_bias, const float *D,
+                const void *z, int64_t z_stride, void *state, int state_dtype,
+                int64_t slot_stride, int32_t P, void *out, const int32_t *state_indices,
+                int32_t batch, int32_t active_batch, int32_t channels, int32_t ngroups,
+                int32_t dstate, int dt_softplus, int32_t *err_flags, ssu_stream_t stream);
+
+/*
+ * spec_verify -- which drafted tokens the target accepts, and the token that follows them:
+ * the step between a verification pass (ssu_prefill with the stash, ssu_ddtree,
+ * scan_prefill) and the commit (ssu_replay, ssu_conv_replay), whose accepted_lengths and
+ * accepted_node_ids it writes. Random numbers are inputs; the same inputs give the same
+ * tokens. A row's tokens are those fed to the verification: tokens[b][0] (a tree's root) is
+ * already decided, the others are drafted; row t of target_probs is the target's
+ * distribution of the token after tokens[b][t].
+ *   Chain (tree_parent_ids NULL), L_b = context_lengths[b] tokens (T when NULL): for
+ *   t = 0, 1, .., L_b - 2 the token x = tokens[b][t+1] is accepted while
+ *       uniforms[b][t] * q[t][x] < p[t][x]      (q = draft_probs, or 1 when NULL),
+ *   in exact arithmetic. accepted_lengths[b] = 1 + the number accepted (so it counts
+ *   tokens[b][0]) and the next token is drawn from row accepted_lengths[b] - 1: from
+ *   max(p - q, 0) after a rejection (from p without the rejected token when draft_probs is
+ *   NULL), from p when all were accepted. If that residual holds no mass, from p.
+ *   Tree (tree_parent_ids [batch, T] as in ssu_ddtree, T <= 128, draft_probs NULL), over the
+ *   row's first L_b nodes: from the root (the first node with parent -1; others are never
+ *   accepted), at node i the first child in node order whose running sum of
+ *   p[i][token of the child] over the children so far exceeds uniforms[b][i] is accepted (a
+ *   token that an earlier sibling has adds nothing and is not accepted again). Where none
+ *   is, the next token is drawn from p[i] without the children's tokens. A path that reaches
+ *   max_accept_len nodes ends there and the next token is drawn from p of its last node.
+ *   Drawing: the first token (in token order) at which the running sum of masses exceeds
+ *   uniform_sample[b] times their total, summed in 64 bits; the last token with mass where
+ *   none does. Only positive finite probabilities have mass; p and q need not sum to 1.
+ *   tokens           [batch, T] int32
+ *   target_probs     [batch, T, vocab] p_dtype, rows target_stride elements apart
+ *   draft_probs      [batch, T-1, vocab] p_dtype (optional), rows draft_stride apart: row t
+ *                    is the distribution tokens[b][t+1] was drawn from
+ *   uniforms         [batch, T] fp32 in [0, 1);  uniform_sample [batch] fp32 in [0, 1)
+ *   state_indices    [batch] int32 (optional): a negative index marks a padding row
+ *   accepted_lengths [batch], next_tokens [batch] int32 (written; 0 and -1 for a padding row,
+ *                    for L_b == 0 and for a tree without a root)
+ *   accepted_node_ids [batch, max_accept_len] int32 (optional, trees only): the path, -1
+ *                    beyond it
+ * Flags: SSU_FLAG_TOKEN (a drafted token outside [0, vocab), never accepted), SSU_FLAG_TREE
+ * (a parent outside [-1, L_b), or no root: the node is never accepted), SSU_FLAG_NO_MASS
+ * (p itself holds no mass: next token -1), and the length flags. One launch.
+ */
+int spec_verify(const int32_t *tokens, const void *target_probs, const void *draft_probs,
+                int p_dtype, int64_t target_stride, int64_t draft_stride, const float *uniforms,
+                const float *uniform_sample, const int32_t *context_lengths,
+                const int32_t *tree_parent_ids, const int32_t *state_indices,
+                int32_t *accepted_lengths, int32_t *next_tokens, int32_t *accepted_node_ids,
+                int32_t max_accept_len, int32_t batch, int32_t active_batch, int32_t T,
+                int32_t vocab, int32_t *err_flags, ssu_stream_t stream);
 
 /*
  * gdn_decode -- one gated delta-rule decode token over a paged fp32 state pool.

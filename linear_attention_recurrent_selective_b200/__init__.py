@@ -16,7 +16,12 @@ from .ssu import (  # noqa: F401
     pool_copy_slot,
     pool_gather,
     pool_scatter,
+    scan_decode,
+    scan_prefill,
+    spec_verify,
     ssu_conv_decode,
+    ssu_conv_prefill,
+    ssu_conv_replay,
     ssu_ddtree,
     ssu_decode,
     ssu_prefill,

@@ -59,6 +59,84 @@ int check_pool_alignment(const void *state, int state_dtype, int64_t slot_stride
     return SSU_OK;
 }
 
+// The conv pool's strides: every (channel, tap) of a slot lies inside the slot's extent,
+// and no two of them share an element.
+int check_conv_pool(int64_t slot_stride, int64_t stride_c, int64_t stride_k, int64_t channels,
+                    int32_t width)
+{
+    if (width < 1 || width > 16)
+        return SSU_ERR_SHAPE;
+    if (width == 1)
+        return SSU_OK;
+    const int64_t taps = width - 1;
+    if (stride_c < 1 || (taps > 1 && stride_k < 1) || stride_k < 0)
+        return SSU_ERR_SHAPE;
+    // (the products below stay in 64 bits)
+    if (slot_stride < 1 || slot_stride > (int64_t)1 << 40 || stride_k > slot_stride ||
+        stride_c > slot_stride / (channels > 1 ? channels - 1 : 1))
+        return SSU_ERR_SHAPE;
+    if ((channels - 1) * stride_c + (taps - 1) * stride_k >= slot_stride)
+        return SSU_ERR_SHAPE;
+    if (taps > 1 && channels > 1 && stride_c < taps * stride_k && stride_k < channels * stride_c)
+        return SSU_ERR_SHAPE;
+    return SSU_OK;
+}
+
+int check_scan(int x_dtype, int64_t x_stride, int dt_dtype, int64_t dt_stride, int bc_dtype,
+               int64_t B_stride, int64_t C_stride, bool gated, int64_t z_stride, int state_dtype,
+               int64_t slot_stride, int32_t P, const int32_t *idx, int32_t batch, int32_t active,
+               int32_t channels, int32_t groups, int32_t N)
+{
+    if (!valid_dtype(x_dtype) || !valid_dtype(dt_dtype) || !valid_dtype(bc_dtype))
+        return SSU_ERR_DTYPE;
+    // a pool [P, channels, dstate] is one of channels heads of one row each
+    int rc = check_sizes(state_dtype, slot_stride, P, idx, batch, active, channels, groups, 1, N);
+    if (rc != SSU_OK)
+        return rc;
+    const int64_t bc = (int64_t)groups * N;
+    if (x_stride < channels || dt_stride < channels || (gated && z_stride < channels) ||
+        B_stride < bc || C_stride < bc)
+        return SSU_ERR_SHAPE;
+    return SSU_OK;
+}
+
+void pack_scan(ssu::ScanArgs &a, const void *x, int x_dtype, int64_t x_stride, const void *dt,
+               int dt_dtype, int64_t dt_stride, const float *A, const void *B, const void *C,
+               int bc_dtype, int64_t B_stride, int64_t C_stride, const float *dt_bias,
+               const float *D, const void *z, int64_t z_stride, void *state, int state_dtype,
+               int64_t slot_stride, int32_t P, void *out, const int32_t *idx, int32_t active,
+               int32_t channels, int32_t groups, int32_t N, int softplus, int32_t *err)
+{
+    a.x = x;
+    a.dt = dt;
+    a.z = z;
+    a.A = A;
+    a.B = B;
+    a.C = C;
+    a.dt_bias = dt_bias;
+    a.Dp = D;
+    a.state = state;
+    a.out = out;
+    a.idx = idx;
+    a.err = err;
+    a.ldx = x_stride;
+    a.lddt = dt_stride;
+    a.ldz = z_stride;
+    a.ldb = B_stride;
+    a.ldc = C_stride;
+    a.slot_stride = slot_stride;
+    a.P = P;
+    a.active = active;
+    a.D = channels;
+    a.G = groups;
+    a.N = N;
+    a.x_dtype = x_dtype;
+    a.dt_dtype = dt_dtype;
+    a.bc_dtype = bc_dtype;
+    a.state_dtype = state_dtype;
+    a.softplus = softplus ? 1 : 0;
+}
+
 ssu::DecodeArgs pack_decode(const void *x, int x_dtype, const float *A, const void *B,
                             const void *C, int bc_dtype, const float *dt,
                             const float *dt_bias, const float *D, const void *z,
@@ -287,6 +365,210 @@ int ssu_conv_decode(const void *xbc, int x_dtype, const void *conv_weight,
     a.width = width;
     a.silu = conv_silu ? 1 : 0;
     return ssu::launch_conv_decode(a, state_dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int ssu_conv_prefill(const void *xbc, int x_dtype, int64_t xbc_stride, const void *conv_weight,
+                     const void *conv_bias, void *conv_state, int64_t conv_slot_stride,
+                     int64_t conv_stride_c, int64_t conv_stride_k, int32_t width, int conv_silu,
+                     int32_t P, void *x, void *B, void *C, const int32_t *state_indices,
+                     const int32_t *context_lengths, const int32_t *tree_parent_ids,
+                     int update_state, int32_t batch, int32_t active_batch, int32_t T,
+                     int32_t x_dim, int32_t bc_dim, int32_t *err_flags, ssu_stream_t stream)
+{
+    if (!valid_dtype(x_dtype))
+        return SSU_ERR_DTYPE;
+    if (batch < 0 || active_batch < 0 || active_batch > batch || P < 0 || T < 0)
+        return SSU_ERR_SHAPE;
+    if (x_dim <= 0 || bc_dim < 0)
+        return SSU_ERR_SHAPE;
+    const int64_t cd = (int64_t)x_dim + 2 * (int64_t)bc_dim;
+    if (cd > 0x7fffffffLL || xbc_stride < cd)
+        return SSU_ERR_SHAPE;
+    int rc = check_conv_pool(conv_slot_stride, conv_stride_c, conv_stride_k, cd, width);
+    if (rc != SSU_OK)
+        return rc;
+    if (!state_indices && active_batch > P)
+        return SSU_ERR_SHAPE;
+    if (tree_parent_ids && update_state)      // a tree's tokens enter by ssu_conv_replay
+        return SSU_ERR_SHAPE;
+    if (active_batch == 0 || T == 0)
+        return SSU_OK;
+    if (!xbc || !conv_weight || !x || (bc_dim > 0 && (!B || !C)) || (width > 1 && !conv_state))
+        return SSU_ERR_NULL;
+    ssu::ConvPrefillArgs a = {};
+    a.xbc = xbc;
+    a.w = conv_weight;
+    a.bias = conv_bias;
+    a.cstate = conv_state;
+    a.x = x;
+    a.B = bc_dim > 0 ? B : nullptr;
+    a.C = bc_dim > 0 ? C : nullptr;
+    a.idx = state_indices;
+    a.ctx = context_lengths;
+    a.parents = tree_parent_ids;
+    a.err = err_flags;
+    a.ldx = xbc_stride;
+    a.cslot = conv_slot_stride;
+    a.cc = conv_stride_c;
+    a.ck = conv_stride_k;
+    a.P = P;
+    a.active = active_batch;
+    a.T = T;
+    a.x_dim = x_dim;
+    a.bc_dim = bc_dim;
+    a.width = width;
+    a.silu = conv_silu ? 1 : 0;
+    a.update = update_state && width > 1 ? 1 : 0;
+    return ssu::launch_conv_prefill(a, x_dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int ssu_conv_replay(const void *xbc, int x_dtype, int64_t xbc_stride, void *conv_state,
+                    int64_t conv_slot_stride, int64_t conv_stride_c, int64_t conv_stride_k,
+                    int32_t width, int32_t P, const int32_t *accepted_lengths,
+                    const int32_t *state_indices, int32_t batch, int32_t active_batch, int32_t T,
+                    int32_t conv_dim, const int32_t *accepted_node_ids, int32_t max_accept_len,
+                    int32_t *err_flags, ssu_stream_t stream)
+{
+    if (!valid_dtype(x_dtype))
+        return SSU_ERR_DTYPE;
+    if (batch < 0 || active_batch < 0 || active_batch > batch || P < 0 || T < 0)
+        return SSU_ERR_SHAPE;
+    if (conv_dim <= 0 || xbc_stride < conv_dim || (accepted_node_ids && max_accept_len < 0))
+        return SSU_ERR_SHAPE;
+    int rc = check_conv_pool(conv_slot_stride, conv_stride_c, conv_stride_k, conv_dim, width);
+    if (rc != SSU_OK)
+        return rc;
+    if (!state_indices && active_batch > P)
+        return SSU_ERR_SHAPE;
+    if (active_batch == 0 || T == 0 || width == 1)
+        return SSU_OK;
+    if (!xbc || !conv_state || !accepted_lengths)
+        return SSU_ERR_NULL;
+    ssu::ConvPrefillArgs a = {};
+    a.xbc = xbc;
+    a.cstate = conv_state;
+    a.idx = state_indices;
+    a.ctx = accepted_lengths;
+    a.nodes = accepted_node_ids;
+    a.err = err_flags;
+    a.ldx = xbc_stride;
+    a.cslot = conv_slot_stride;
+    a.cc = conv_stride_c;
+    a.ck = conv_stride_k;
+    a.P = P;
+    a.active = active_batch;
+    a.T = T;
+    a.x_dim = conv_dim;
+    a.width = width;
+    a.max_accept = max_accept_len;
+    return ssu::launch_conv_replay(a, x_dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int scan_prefill(const void *x, int x_dtype, int64_t x_stride, const void *dt, int dt_dtype,
+                 int64_t dt_stride, const float *A, const void *B, const void *C, int bc_dtype,
+                 int64_t B_stride, int64_t C_stride, const float *dt_bias, const float *D,
+                 const void *z, int64_t z_stride, void *state, int state_dtype,
+                 int64_t slot_stride, int32_t P, void *out, const int32_t *state_indices,
+                 const int32_t *context_lengths, int update_state, int32_t batch,
+                 int32_t active_batch, int32_t T, int32_t channels, int32_t ngroups,
+                 int32_t dstate, int dt_softplus, int32_t *err_flags, ssu_stream_t stream)
+{
+    if (T < 0)
+        return SSU_ERR_SHAPE;
+    ssu::ScanArgs a = {};
+    int rc = check_scan(x_dtype, x_stride, dt_dtype, dt_stride, bc_dtype, B_stride, C_stride,
+                        z != nullptr, z_stride, state_dtype, slot_stride, P, state_indices, batch,
+                        active_batch, channels, ngroups, dstate);
+    if (rc != SSU_OK || active_batch == 0 || T == 0)
+        return rc;
+    if (!x || !dt || !A || !B || !state || (out && !C) || (!out && !update_state))
+        return SSU_ERR_NULL;
+    if ((rc = check_pool_alignment(state, state_dtype, slot_stride)) != SSU_OK)
+        return rc;
+    if (!aligned16(A))
+        return SSU_ERR_ALIGN;
+    pack_scan(a, x, x_dtype, x_stride, dt, dt_dtype, dt_stride, A, B, C, bc_dtype, B_stride,
+              C_stride, dt_bias, D, z, z_stride, state, state_dtype, slot_stride, P, out,
+              state_indices, active_batch, channels, ngroups, dstate, dt_softplus, err_flags);
+    a.ctx = context_lengths;
+    a.T = T;
+    a.update = update_state ? 1 : 0;
+    return ssu::launch_scan_prefill(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int scan_decode(const void *x, int x_dtype, int64_t x_stride, const void *dt, int dt_dtype,
+                int64_t dt_stride, const float *A, const void *B, const void *C, int bc_dtype,
+                int64_t B_stride, int64_t C_stride, const float *dt_bias, const float *D,
+                const void *z, int64_t z_stride, void *state, int state_dtype,
+                int64_t slot_stride, int32_t P, void *out, const int32_t *state_indices,
+                int32_t batch, int32_t active_batch, int32_t channels, int32_t ngroups,
+                int32_t dstate, int dt_softplus, int32_t *err_flags, ssu_stream_t stream)
+{
+    ssu::ScanArgs a = {};
+    int rc = check_scan(x_dtype, x_stride, dt_dtype, dt_stride, bc_dtype, B_stride, C_stride,
+                        z != nullptr, z_stride, state_dtype, slot_stride, P, state_indices, batch,
+                        active_batch, channels, ngroups, dstate);
+    if (rc != SSU_OK || active_batch == 0)
+        return rc;
+    if (!x || !dt || !A || !B || !C || !state || !out)
+        return SSU_ERR_NULL;
+    if ((rc = check_pool_alignment(state, state_dtype, slot_stride)) != SSU_OK)
+        return rc;
+    if (!aligned16(A))
+        return SSU_ERR_ALIGN;
+    pack_scan(a, x, x_dtype, x_stride, dt, dt_dtype, dt_stride, A, B, C, bc_dtype, B_stride,
+              C_stride, dt_bias, D, z, z_stride, state, state_dtype, slot_stride, P, out,
+              state_indices, active_batch, channels, ngroups, dstate, dt_softplus, err_flags);
+    a.T = 1;
+    a.update = 1;
+    return ssu::launch_scan_decode(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int spec_verify(const int32_t *tokens, const void *target_probs, const void *draft_probs,
+                int p_dtype, int64_t target_stride, int64_t draft_stride, const float *uniforms,
+                const float *uniform_sample, const int32_t *context_lengths,
+                const int32_t *tree_parent_ids, const int32_t *state_indices,
+                int32_t *accepted_lengths, int32_t *next_tokens, int32_t *accepted_node_ids,
+                int32_t max_accept_len, int32_t batch, int32_t active_batch, int32_t T,
+                int32_t vocab, int32_t *err_flags, ssu_stream_t stream)
+{
+    if (!valid_dtype(p_dtype))
+        return SSU_ERR_DTYPE;
+    if (batch < 0 || active_batch < 0 || active_batch > batch || T < 0)
+        return SSU_ERR_SHAPE;
+    if (vocab <= 0 || vocab > (1 << 30) || target_stride < vocab)
+        return SSU_ERR_SHAPE;
+    if (draft_probs && (tree_parent_ids || draft_stride < vocab))
+        return SSU_ERR_SHAPE;
+    if (tree_parent_ids && T > 128)
+        return SSU_ERR_SHAPE;
+    if (accepted_node_ids && (!tree_parent_ids || max_accept_len < 1))
+        return SSU_ERR_SHAPE;
+    if (active_batch == 0 || T == 0)
+        return SSU_OK;
+    if (!tokens || !target_probs || !uniforms || !uniform_sample || !accepted_lengths ||
+        !next_tokens)
+        return SSU_ERR_NULL;
+    ssu::VerifyArgs a = {};
+    a.tokens = tokens;
+    a.p = target_probs;
+    a.q = T > 1 ? draft_probs : nullptr;
+    a.u = uniforms;
+    a.u_sample = uniform_sample;
+    a.ctx = context_lengths;
+    a.parents = tree_parent_ids;
+    a.idx = state_indices;
+    a.accepted = accepted_lengths;
+    a.next = next_tokens;
+    a.nodes = accepted_node_ids;
+    a.err = err_flags;
+    a.ldp = target_stride;
+    a.ldq = draft_stride;
+    a.active = active_batch;
+    a.T = T;
+    a.V = vocab;
+    a.max_accept = max_accept_len;
+    return ssu::launch_verify(a, p_dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int gdn_decode(const void *q, const void *k, const void *v, int x_dtype, const void *a,

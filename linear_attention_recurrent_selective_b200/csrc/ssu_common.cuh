@@ -192,6 +192,54 @@ struct ConvArgs {
     int32_t width, silu;
 };
 
+struct ConvPrefillArgs {
+    const void *xbc;          // [batch, T, channels] raw channels, tokens ldx elements apart
+    const void *w;            // [channels, width], x dtype (NULL in the commit)
+    const void *bias;         // [channels] or NULL, x dtype
+    void *cstate;             // conv pool, element (s, c, k) at s*cslot + c*cc + k*ck
+    void *x, *B, *C;          // dense outputs [batch, T, x_dim], [batch, T, bc_dim]
+    const int32_t *idx;
+    const int32_t *ctx;       // contextLengths (the commit: acceptedLengths) or NULL
+    const int32_t *parents;   // treeParentIds [batch, T] or NULL
+    const int32_t *nodes;     // the commit: acceptedNodeIds [batch, max_accept] or NULL
+    int32_t *err;
+    int64_t ldx, cslot, cc, ck;
+    int32_t P, active, T, x_dim, bc_dim, width, silu, update, max_accept;
+    int32_t win_mode;         // set by the launcher: how window taps are accessed
+};
+
+struct ScanArgs {
+    const void *x, *dt, *z;   // [batch, (T,) D], tokens ldx / lddt / ldz elements apart
+    const float *A;           // [D, N]
+    const void *B, *C;        // [batch, (T,) G, N], tokens ldb / ldc elements apart
+    const float *dt_bias, *Dp;  // [D] or NULL
+    void *state;              // pool [P, D, N]
+    void *out;                // [batch, (T,) D] dense, or NULL (prefill: advance only)
+    const int32_t *idx;
+    const int32_t *ctx;       // contextLengths [batch] or NULL
+    int32_t *err;
+    int64_t ldx, lddt, ldz, ldb, ldc, slot_stride;
+    int32_t P, active, T, D, G, N;
+    int x_dtype, dt_dtype, bc_dtype, state_dtype, softplus, update;
+    int vec;                  // set by the launcher: which rows take 16-byte accesses
+};
+
+struct VerifyArgs {
+    const int32_t *tokens;    // [batch, T]
+    const void *p, *q;        // target rows [batch, T, V]; draft rows [batch, T-1, V] or NULL
+    const float *u;           // [batch, T]
+    const float *u_sample;    // [batch]
+    const int32_t *ctx;       // contextLengths [batch] or NULL
+    const int32_t *parents;   // treeParentIds [batch, T] or NULL (a chain)
+    const int32_t *idx;       // state_indices [batch] or NULL: only their sign is used
+    int32_t *accepted;        // [batch]
+    int32_t *next;            // [batch]
+    int32_t *nodes;           // acceptedNodeIds [batch, max_accept] or NULL
+    int32_t *err;
+    int64_t ldp, ldq;         // elements between rows of p and of q
+    int32_t active, T, V, max_accept;
+};
+
 struct GdnArgs {
     const void *q, *k;        // [batch, HK, K], x dtype
     const void *v;            // [batch, HV, V], x dtype
@@ -222,6 +270,11 @@ int launch_prefill_tc(const PrefillArgs &a, int state_dtype, cudaStream_t s);  /
 int launch_replay(const ReplayArgs &a, int state_dtype, cudaStream_t s);
 int launch_ddtree(const TreeArgs &a, int state_dtype, cudaStream_t s);
 int launch_conv_decode(const ConvArgs &a, int state_dtype, cudaStream_t s);
+int launch_conv_prefill(const ConvPrefillArgs &a, int x_dtype, cudaStream_t s);
+int launch_conv_replay(const ConvPrefillArgs &a, int x_dtype, cudaStream_t s);
+int launch_scan_decode(const ScanArgs &a, cudaStream_t s);
+int launch_scan_prefill(ScanArgs a, cudaStream_t s);
+int launch_verify(const VerifyArgs &a, int p_dtype, cudaStream_t s);
 int launch_gdn_decode(const GdnArgs &a, cudaStream_t s);
 int launch_clear(void *pool, int64_t bytes, cudaStream_t s);
 int launch_copy(void *dst, const void *src, int64_t bytes, cudaStream_t s);

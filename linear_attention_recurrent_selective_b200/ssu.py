@@ -13,6 +13,12 @@ Semantics (Selective State Update page of the TensorRT-Edge-LLM C++ API):
                (invokeSelectiveStateUpdatePrefill)
   ssu_conv_decode  causal conv1d update of the raw xBC channels fused with the decode
                (convState beside the recurrent state; FlashInfer conv update)
+  ssu_conv_prefill  the same causal conv1d over the tokens of a prompt or a draft tree, as
+               x, B and C tensors; ssu_conv_replay commits accepted tokens to the windows
+  scan_prefill / scan_decode  the selective scan with a step per channel and a decay per
+               (channel, state), over prompts and single tokens
+  spec_verify  which drafted tokens the target accepts and the token that follows, from
+               given random numbers
   gdn_decode   gated delta-rule decode core over a paged fp32 pool (FlashInfer GDN page)
   ssu_ddtree   tree verify: every node of a draft tree from the committed state along its
                ancestor path, stash per node (invokeSelectiveStateUpdateDDTree)
@@ -25,6 +31,7 @@ Semantics (Selective State Update page of the TensorRT-Edge-LLM C++ API):
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -43,10 +50,13 @@ FLAG_TIMEOUT = 16
 FLAG_LAYER = 32
 FLAG_TREE = 64
 FLAG_DUPLICATE_INDEX = 128
+FLAG_TOKEN = 256
+FLAG_NO_MASS = 512
 
 # Every C entry point declared in include/ssu.h, in declaration order.
 ENTRY_POINTS = ("ssu_decode", "ssu_prefill", "ssu_replay", "ssu_replay_layers",
-                "ssu_conv_decode", "gdn_decode", "ssu_ddtree", "pool_clear_slot",
+                "ssu_conv_decode", "ssu_conv_prefill", "ssu_conv_replay", "scan_prefill",
+                "scan_decode", "spec_verify", "gdn_decode", "ssu_ddtree", "pool_clear_slot",
                 "pool_copy_slot", "pool_clear_slot_layers", "pool_gather", "pool_scatter",
                 "ssu_check_state_indices", "ssu_status_string")
 
@@ -101,6 +111,16 @@ def load(path: str) -> ctypes.CDLL:
     L.ssu_conv_decode.argtypes = [vp, ci, vp, vp, vp, i64, i64, i64, i32, ci, vp, vp, vp, vp,
                                   vp, vp, ci, i64, i32, vp, vp, i32, i32, i32, i32, i32, i32,
                                   ci, vp, vp]
+    L.ssu_conv_prefill.argtypes = [vp, ci, i64, vp, vp, vp, i64, i64, i64, i32, ci, i32, vp, vp,
+                                   vp, vp, vp, vp, ci, i32, i32, i32, i32, i32, vp, vp]
+    L.ssu_conv_replay.argtypes = [vp, ci, i64, vp, i64, i64, i64, i32, i32, vp, vp, i32, i32,
+                                  i32, i32, vp, i32, vp, vp]
+    scan = [vp, ci, i64, vp, ci, i64, vp, vp, vp, ci, i64, i64, vp, vp, vp, i64, vp, ci, i64, i32,
+            vp, vp]
+    L.scan_prefill.argtypes = scan + [vp, ci, i32, i32, i32, i32, i32, i32, ci, vp, vp]
+    L.scan_decode.argtypes = scan + [i32, i32, i32, i32, i32, ci, vp, vp]
+    L.spec_verify.argtypes = [vp, vp, vp, ci, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32,
+                              i32, i32, i32, vp, vp]
     L.gdn_decode.argtypes = [vp, vp, vp, ci, vp, vp, vp, vp, ctypes.c_float, ci, vp, i64, i32,
                              vp, vp, i32, i32, i32, i32, i32, i32, vp, vp]
     L.ssu_ddtree.argtypes = [vp, ci, vp, vp, vp, ci, vp, vp, vp, vp, ci, i64, i32, vp, vp, vp,
@@ -333,6 +353,274 @@ def ssu_conv_decode(xbc, conv_weight, conv_state, A, dt, state, out, *, width, c
         int(bool(dt_softplus)), _ptr(err_flags, "err_flags", torch.int32), _stream(stream))
     _check("ssu_conv_decode", rc)
     return out
+
+
+def _common_device(first, *others):
+    """The CUDA device that every given tensor lives on (None entries are skipped)."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got one on {dev}")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and on {t.device} in one call")
+    return dev
+
+
+def _run(fn, device, stream, *args):
+    """Call the C entry point ``fn`` on ``stream`` (the current one of the tensors' device
+    when None), with that device current for the launch."""
+    f = getattr(_lib or lib(), fn)
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream of {stream.device} given for tensors on {device}")
+    if torch.cuda.current_device() == device.index:
+        rc = f(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args, stream.cuda_stream)
+    if rc:
+        _check(fn, rc)
+
+
+def _vector(t, name, n, dtype=torch.int32):
+    """Pointer of a dense [n] tensor of ``dtype`` (None stays NULL)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a dense [{n}] tensor of {dtype}, got "
+                         f"{list(t.shape)} of {t.dtype}")
+    return t.data_ptr()
+
+
+def _dense(t, name, shape, dtype):
+    """Pointer of a contiguous tensor of ``shape`` and ``dtype`` (None stays NULL)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {list(shape)} of {dtype}, got "
+                         f"{list(t.shape)} of {t.dtype}")
+    return t.data_ptr()
+
+
+def _tokens(t, name, lead, inner):
+    """Elements between consecutive tokens of ``t`` [*lead, *inner]: each token's ``inner``
+    block is dense, the tokens of all rows are equally far apart (a slice of wider rows)."""
+    if tuple(t.shape) != tuple(lead) + tuple(inner):
+        raise ValueError(f"{name} must be {list(lead) + list(inner)}, got {list(t.shape)}")
+    k, size, step, far = len(lead), t.shape, t.stride(), 1
+    for i in range(len(size) - 1, k - 1, -1):
+        if size[i] != 1 and step[i] != far:
+            raise ValueError(f"{name}: a token's elements must be dense")
+        far *= size[i]
+    if k == 1:
+        return step[0] if size[0] > 1 else far
+    if size[1] > 1:
+        if size[0] > 1 and step[0] != size[1] * step[1]:
+            raise ValueError(f"{name}: rows must follow one another, T tokens apart")
+        return step[1]
+    return step[0] if size[0] > 1 else far
+
+
+def _extent(t):
+    """Elements of storage from a tensor's first element to its last one."""
+    return 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())) if t.numel() else 0
+
+
+def _conv_pool(conv_state, conv_strides, channels, width, dtype, P):
+    """(pointer, slot, channel and tap strides, P) of a conv pool; the tensor must reach
+    over every slot's taps."""
+    if width <= 1 or conv_state is None:
+        return None, 0, 0, 0, (P if P is not None else 2 ** 31 - 1)
+    if conv_state.dtype != dtype:
+        raise ValueError("conv_state must have xbc's dtype")
+    cs, cc, ck = conv_strides
+    if P is None:
+        P = conv_state.shape[0] if conv_state.dim() == 3 else conv_state.numel() // max(cs, 1)
+    if P > 0:
+        last = (P - 1) * cs + (channels - 1) * cc + (width - 2) * ck
+        if last >= _extent(conv_state):
+            raise ValueError(f"conv_state does not hold {P} slots with strides {conv_strides}")
+    return conv_state.data_ptr(), cs, cc, ck, P
+
+
+def ssu_conv_prefill(xbc, conv_weight, conv_state, x, B=None, C=None, *, width, conv_strides,
+                     conv_bias=None, conv_silu=True, state_indices=None, context_lengths=None,
+                     parent_ids=None, update_state=True, active_batch=None, err_flags=None,
+                     P=None, stream=None):
+    """Causal conv1d of the raw channels xbc [batch, T, conv_dim] (tokens may be slices of
+    wider rows) from the slots' windows, into the dense outputs x [batch, T, x_dim (or H, Dm)]
+    and B, C [batch, T, bc_dim (or G, N)] (None: no such channels). conv_state and
+    conv_strides as in ssu_conv_decode. ``update_state`` advances the windows by the row's
+    tokens; with ``parent_ids`` [batch, T] the tokens are the nodes of draft trees
+    (update_state must be off: commit with ssu_conv_replay)."""
+    dev = _common_device(xbc, conv_weight, conv_state, x, B, C, conv_bias, state_indices,
+                         context_lengths, parent_ids, err_flags)
+    batch, T, ch = xbc.shape
+    active = batch if active_batch is None else active_batch
+    ld = _tokens(xbc, "xbc", (batch, T), (ch,))
+    dt = xbc.dtype
+    dims = []
+    for t, name in ((x, "x"), (B, "B"), (C, "C")):
+        if t is None:
+            dims.append(0)
+            continue
+        if t.dtype != dt or tuple(t.shape[:2]) != (batch, T) or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous [batch, T, ...] in xbc's dtype")
+        dims.append(math.prod(t.shape[2:]))
+    if dims[1] != dims[2] or dims[0] + 2 * dims[1] != ch:
+        raise ValueError(f"x, B and C hold {dims} channels, xbc {ch}")
+    pool, cs, cc, ck, P = _conv_pool(conv_state, conv_strides, ch, width, dt, P)
+    _debug_indices(state_indices, P, active, stream)
+    _run("ssu_conv_prefill", dev, stream, xbc.data_ptr(), _dt(xbc, "xbc"), ld,
+         _dense(conv_weight, "conv_weight", (ch, width), dt),
+         _vector(conv_bias, "conv_bias", ch, dt), pool, cs, cc, ck, width, int(bool(conv_silu)),
+         P, x.data_ptr(), None if B is None else B.data_ptr(), None if C is None else C.data_ptr(),
+         _vector(state_indices, "state_indices", batch),
+         _vector(context_lengths, "context_lengths", batch),
+         _dense(parent_ids, "parent_ids", (batch, T), torch.int32), int(bool(update_state)),
+         batch, active, T, dims[0], dims[1], _vector(err_flags, "err_flags", 1))
+    return x, B, C
+
+
+def ssu_conv_replay(xbc, conv_state, accepted_lengths, *, width, conv_strides,
+                    state_indices=None, accepted_node_ids=None, active_batch=None,
+                    err_flags=None, P=None, stream=None):
+    """Commit the first accepted_lengths[b] tokens of xbc [batch, T, conv_dim] (or the nodes
+    accepted_node_ids[b, :accepted_lengths[b]]) to the conv windows, as ssu_replay commits
+    them to the recurrent state."""
+    dev = _common_device(xbc, conv_state, accepted_lengths, state_indices, accepted_node_ids,
+                         err_flags)
+    batch, T, ch = xbc.shape
+    active = batch if active_batch is None else active_batch
+    ld = _tokens(xbc, "xbc", (batch, T), (ch,))
+    pool, cs, cc, ck, P = _conv_pool(conv_state, conv_strides, ch, width, xbc.dtype, P)
+    ids, most = None, 0
+    if accepted_node_ids is not None:
+        if accepted_node_ids.dim() != 2:
+            raise ValueError("accepted_node_ids must be [batch, maxAcceptLen]")
+        most = accepted_node_ids.shape[1]
+        ids = _dense(accepted_node_ids, "accepted_node_ids", (batch, most), torch.int32)
+    _debug_indices(state_indices, P, active, stream)
+    _run("ssu_conv_replay", dev, stream, xbc.data_ptr(), _dt(xbc, "xbc"), ld, pool, cs, cc, ck,
+         width, P, _vector(accepted_lengths, "accepted_lengths", batch),
+         _vector(state_indices, "state_indices", batch), batch, active, T, ch, ids, most,
+         _vector(err_flags, "err_flags", 1))
+
+
+def _scan_args(lead, x, dt, A, B, C, state, out, D, z, dt_bias, state_indices, context_lengths,
+               err_flags, slot_stride, P):
+    """The arguments scan_prefill and scan_decode share, up to state_indices."""
+    dev = _common_device(x, dt, A, B, C, state, out, D, z, dt_bias, state_indices,
+                         context_lengths, err_flags)
+    ch = x.shape[-1]
+    G, N = B.shape[-2:]
+    if out is not None and (out.dtype != x.dtype or out.shape != x.shape or
+                            not out.is_contiguous()):
+        raise ValueError("out must be contiguous, in x's shape and dtype")
+    if z is not None and z.dtype != x.dtype:
+        raise ValueError("z must have x's dtype")
+    if C is not None and C.dtype != B.dtype:
+        raise ValueError("C must have B's dtype")
+    if state.dim() == 3:
+        if tuple(state.shape[1:]) != (ch, N) or state.stride(2) != 1 or state.stride(1) != N:
+            raise ValueError(f"state must be [P, {ch}, {N}], contiguous inside a slot")
+        stride = state.stride(0) if slot_stride is None else slot_stride
+        P = state.shape[0] if P is None else P
+    else:
+        if state.dim() != 1 or not state.is_contiguous():
+            raise ValueError("state must be [P, channels, dstate] or flat contiguous storage")
+        stride = ch * N if slot_stride is None else slot_stride
+        P = state.numel() // max(stride, 1) if P is None else P
+    if P > 0 and (P - 1) * stride + ch * N > _extent(state):
+        raise ValueError(f"state does not hold {P} slots of stride {stride}")
+    f32, inner = torch.float32, (ch,)
+    return dev, G, N, P, [
+        x.data_ptr(), _dt(x, "x"), _tokens(x, "x", lead, inner), dt.data_ptr(), _dt(dt, "dt"),
+        _tokens(dt, "dt", lead, inner), _dense(A, "A", (ch, N), f32), B.data_ptr(),
+        None if C is None else C.data_ptr(), _dt(B, "B"), _tokens(B, "B", lead, (G, N)),
+        G * N if C is None else _tokens(C, "C", lead, (G, N)),
+        _vector(dt_bias, "dt_bias", ch, f32), _vector(D, "D", ch, f32),
+        None if z is None else z.data_ptr(), 0 if z is None else _tokens(z, "z", lead, inner),
+        state.data_ptr(), _dt(state, "state"), stride, P,
+        None if out is None else out.data_ptr(),
+        _vector(state_indices, "state_indices", lead[0])]
+
+
+def scan_prefill(x, dt, A, B, C, state, out, *, D=None, z=None, dt_bias=None, dt_softplus=True,
+                 state_indices=None, context_lengths=None, update_state=True, active_batch=None,
+                 err_flags=None, slot_stride=None, P=None, stream=None):
+    """The per-channel selective scan over T tokens. x, z, out [batch, T, channels]; dt
+    [batch, T, channels] (own dtype); A [channels, dstate] fp32; B, C [batch, T, G, dstate];
+    dt_bias, D [channels] fp32; state pool [P, channels, dstate] (or flat with slot_stride).
+    x, dt, z, B and C may be slices of wider rows. ``update_state=False`` only reads the pool;
+    ``out=None`` only advances it (C may then be None)."""
+    batch, T, ch = x.shape
+    active = batch if active_batch is None else active_batch
+    dev, G, N, P, args = _scan_args((batch, T), x, dt, A, B, C, state, out, D, z, dt_bias,
+                                    state_indices, context_lengths, err_flags, slot_stride, P)
+    _debug_indices(state_indices, P, active, stream)
+    _run("scan_prefill", dev, stream, *args, _vector(context_lengths, "context_lengths", batch),
+         int(bool(update_state)), batch, active, T, ch, G, N, int(bool(dt_softplus)),
+         _vector(err_flags, "err_flags", 1))
+    return out
+
+
+def scan_decode(x, dt, A, B, C, state, out, *, D=None, z=None, dt_bias=None, dt_softplus=True,
+                state_indices=None, active_batch=None, err_flags=None, slot_stride=None, P=None,
+                stream=None):
+    """One token of the per-channel selective scan. x, z, out, dt [batch, channels]; B, C
+    [batch, G, dstate]; other arguments as in scan_prefill; the state is updated in place."""
+    batch, ch = x.shape
+    active = batch if active_batch is None else active_batch
+    dev, G, N, P, args = _scan_args((batch,), x, dt, A, B, C, state, out, D, z, dt_bias,
+                                    state_indices, None, err_flags, slot_stride, P)
+    _debug_indices(state_indices, P, active, stream)
+    _run("scan_decode", dev, stream, *args, batch, active, ch, G, N, int(bool(dt_softplus)),
+         _vector(err_flags, "err_flags", 1))
+    return out
+
+
+def spec_verify(tokens, target_probs, uniforms, uniform_sample, accepted_lengths, next_tokens, *,
+                draft_probs=None, parent_ids=None, accepted_node_ids=None, context_lengths=None,
+                state_indices=None, active_batch=None, err_flags=None, stream=None):
+    """Accept drafted tokens against the target's probabilities, and draw the token after
+    them. tokens [batch, T] int32 (the tokens fed to the verification, the first one already
+    decided); target_probs [batch, T, vocab]; uniforms [batch, T] and uniform_sample [batch]
+    fp32 in [0, 1). A chain takes ``draft_probs`` [batch, T-1, vocab] (None: q = 1); a tree
+    ``parent_ids`` [batch, T] and ``accepted_node_ids`` [batch, maxAcceptLen]. Writes
+    accepted_lengths [batch] (for ssu_replay and ssu_conv_replay), next_tokens [batch] and
+    accepted_node_ids."""
+    dev = _common_device(tokens, target_probs, uniforms, uniform_sample, accepted_lengths,
+                         next_tokens, draft_probs, parent_ids, accepted_node_ids,
+                         context_lengths, state_indices, err_flags)
+    batch, T, V = target_probs.shape
+    active = batch if active_batch is None else active_batch
+    ldq = 0
+    if draft_probs is not None:
+        if draft_probs.dtype != target_probs.dtype:
+            raise ValueError("draft_probs must have target_probs' dtype")
+        ldq = _tokens(draft_probs, "draft_probs", (batch, max(T - 1, 0)), (V,))
+    i32, f32 = torch.int32, torch.float32
+    most = 0
+    if accepted_node_ids is not None:
+        if accepted_node_ids.dim() != 2:
+            raise ValueError("accepted_node_ids must be [batch, maxAcceptLen]")
+        most = accepted_node_ids.shape[1]
+    _run("spec_verify", dev, stream, _dense(tokens, "tokens", (batch, T), i32),
+         target_probs.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(),
+         _dt(target_probs, "target_probs"),
+         _tokens(target_probs, "target_probs", (batch, T), (V,)), ldq,
+         _dense(uniforms, "uniforms", (batch, T), f32),
+         _vector(uniform_sample, "uniform_sample", batch, f32),
+         _vector(context_lengths, "context_lengths", batch),
+         _dense(parent_ids, "parent_ids", (batch, T), i32),
+         _vector(state_indices, "state_indices", batch),
+         _vector(accepted_lengths, "accepted_lengths", batch),
+         _vector(next_tokens, "next_tokens", batch),
+         _dense(accepted_node_ids, "accepted_node_ids", (batch, most), i32), most, batch, active,
+         T, V, _vector(err_flags, "err_flags", 1))
+    return accepted_lengths, next_tokens
 
 
 def gdn_decode(q, k, v, a, b, A_log, state, out, *, dt_bias=None, scale=None,
