@@ -355,14 +355,21 @@ def ssu_conv_decode(xbc, conv_weight, conv_state, A, dt, state, out, *, width, c
     return out
 
 
-def _common_device(first, *others):
-    """The CUDA device that every given tensor lives on (None entries are skipped)."""
-    dev = first.device
-    if dev.type != "cuda":
-        raise ValueError(f"expected CUDA tensors, got one on {dev}")
-    for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and on {t.device} in one call")
+# The current device and its current stream without building Stream objects (a call's fixed
+# cost counts for launch-bound ones); the public calls where a torch build lacks them.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_current_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None) or
+                       (lambda index: torch.cuda.current_stream(index).cuda_stream))
+
+
+def _common_device(*tensors):
+    """Index of the CUDA device that every given tensor lives on (None entries are skipped)."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {tensors[0].device} and on {t.device} in one call")
+    if dev < 0:
+        raise ValueError("expected CUDA tensors")
     return dev
 
 
@@ -371,14 +378,16 @@ def _run(fn, device, stream, *args):
     when None), with that device current for the launch."""
     f = getattr(_lib or lib(), fn)
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"stream of {stream.device} given for tensors on {device}")
-    if torch.cuda.current_device() == device.index:
-        rc = f(*args, stream.cuda_stream)
+        raw = _current_raw_stream(device)
+    else:
+        raw = stream.cuda_stream
+        if stream.device.index != device:
+            raise ValueError(f"stream of {stream.device} given for tensors on cuda:{device}")
+    if _current_device() == device:
+        rc = f(*args, raw)
     else:
         with torch.cuda.device(device):
-            rc = f(*args, stream.cuda_stream)
+            rc = f(*args, raw)
     if rc:
         _check(fn, rc)
 
@@ -387,7 +396,7 @@ def _vector(t, name, n, dtype=torch.int32):
     """Pointer of a dense [n] tensor of ``dtype`` (None stays NULL)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a dense [{n}] tensor of {dtype}, got "
                          f"{list(t.shape)} of {t.dtype}")
     return t.data_ptr()
@@ -397,34 +406,38 @@ def _dense(t, name, shape, dtype):
     """Pointer of a contiguous tensor of ``shape`` and ``dtype`` (None stays NULL)."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {list(shape)} of {dtype}, got "
                          f"{list(t.shape)} of {t.dtype}")
     return t.data_ptr()
 
 
-def _tokens(t, name, lead, inner):
-    """Elements between consecutive tokens of ``t`` [*lead, *inner]: each token's ``inner``
-    block is dense, the tokens of all rows are equally far apart (a slice of wider rows)."""
-    if tuple(t.shape) != tuple(lead) + tuple(inner):
-        raise ValueError(f"{name} must be {list(lead) + list(inner)}, got {list(t.shape)}")
-    k, size, step, far = len(lead), t.shape, t.stride(), 1
-    for i in range(len(size) - 1, k - 1, -1):
-        if size[i] != 1 and step[i] != far:
+def _tokens(t, name, shape, lead, per):
+    """Elements between consecutive tokens of ``t``, whose ``shape`` is ``lead`` (1: rows, 2:
+    rows and tokens) leading sizes and then those of a token of ``per`` elements: each token
+    is dense, and the tokens of all rows are equally far apart (slices of wider rows)."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.is_contiguous():
+        return per
+    step, far = t.stride(), 1
+    for i in range(len(shape) - 1, lead - 1, -1):
+        if shape[i] != 1 and step[i] != far:
             raise ValueError(f"{name}: a token's elements must be dense")
-        far *= size[i]
-    if k == 1:
-        return step[0] if size[0] > 1 else far
-    if size[1] > 1:
-        if size[0] > 1 and step[0] != size[1] * step[1]:
+        far *= shape[i]
+    if lead == 2 and shape[1] > 1:
+        if shape[0] > 1 and step[0] != shape[1] * step[1]:
             raise ValueError(f"{name}: rows must follow one another, T tokens apart")
         return step[1]
-    return step[0] if size[0] > 1 else far
+    return step[0] if shape[0] > 1 else far
 
 
 def _extent(t):
     """Elements of storage from a tensor's first element to its last one."""
-    return 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())) if t.numel() else 0
+    n = t.numel()
+    if n == 0 or t.is_contiguous():
+        return n
+    return 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
 
 
 def _conv_pool(conv_state, conv_strides, channels, width, dtype, P):
@@ -432,7 +445,7 @@ def _conv_pool(conv_state, conv_strides, channels, width, dtype, P):
     over every slot's taps."""
     if width <= 1 or conv_state is None:
         return None, 0, 0, 0, (P if P is not None else 2 ** 31 - 1)
-    if conv_state.dtype != dtype:
+    if conv_state.dtype is not dtype:
         raise ValueError("conv_state must have xbc's dtype")
     cs, cc, ck = conv_strides
     if P is None:
@@ -442,6 +455,16 @@ def _conv_pool(conv_state, conv_strides, channels, width, dtype, P):
         if last >= _extent(conv_state):
             raise ValueError(f"conv_state does not hold {P} slots with strides {conv_strides}")
     return conv_state.data_ptr(), cs, cc, ck, P
+
+
+def _conv_out(t, name, batch, T, dtype):
+    """(pointer, channels) of an output of the convolution; None has no channels."""
+    if t is None:
+        return None, 0
+    shape = t.shape
+    if t.dtype is not dtype or shape[:2] != (batch, T) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [batch, T, ...] in xbc's dtype")
+    return t.data_ptr(), shape[2] if len(shape) == 3 else math.prod(shape[2:])
 
 
 def ssu_conv_prefill(xbc, conv_weight, conv_state, x, B=None, C=None, *, width, conv_strides,
@@ -458,28 +481,22 @@ def ssu_conv_prefill(xbc, conv_weight, conv_state, x, B=None, C=None, *, width, 
                          context_lengths, parent_ids, err_flags)
     batch, T, ch = xbc.shape
     active = batch if active_batch is None else active_batch
-    ld = _tokens(xbc, "xbc", (batch, T), (ch,))
+    ld = _tokens(xbc, "xbc", (batch, T, ch), 2, ch)
     dt = xbc.dtype
-    dims = []
-    for t, name in ((x, "x"), (B, "B"), (C, "C")):
-        if t is None:
-            dims.append(0)
-            continue
-        if t.dtype != dt or tuple(t.shape[:2]) != (batch, T) or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous [batch, T, ...] in xbc's dtype")
-        dims.append(math.prod(t.shape[2:]))
-    if dims[1] != dims[2] or dims[0] + 2 * dims[1] != ch:
-        raise ValueError(f"x, B and C hold {dims} channels, xbc {ch}")
+    xp, xd = _conv_out(x, "x", batch, T, dt)
+    Bp, bd = _conv_out(B, "B", batch, T, dt)
+    Cp, cd = _conv_out(C, "C", batch, T, dt)
+    if bd != cd or xd + 2 * bd != ch:
+        raise ValueError(f"x, B and C hold {xd}, {bd} and {cd} channels, xbc {ch}")
     pool, cs, cc, ck, P = _conv_pool(conv_state, conv_strides, ch, width, dt, P)
     _debug_indices(state_indices, P, active, stream)
     _run("ssu_conv_prefill", dev, stream, xbc.data_ptr(), _dt(xbc, "xbc"), ld,
          _dense(conv_weight, "conv_weight", (ch, width), dt),
          _vector(conv_bias, "conv_bias", ch, dt), pool, cs, cc, ck, width, int(bool(conv_silu)),
-         P, x.data_ptr(), None if B is None else B.data_ptr(), None if C is None else C.data_ptr(),
-         _vector(state_indices, "state_indices", batch),
+         P, xp, Bp, Cp, _vector(state_indices, "state_indices", batch),
          _vector(context_lengths, "context_lengths", batch),
          _dense(parent_ids, "parent_ids", (batch, T), torch.int32), int(bool(update_state)),
-         batch, active, T, dims[0], dims[1], _vector(err_flags, "err_flags", 1))
+         batch, active, T, xd, bd, _vector(err_flags, "err_flags", 1))
     return x, B, C
 
 
@@ -493,7 +510,7 @@ def ssu_conv_replay(xbc, conv_state, accepted_lengths, *, width, conv_strides,
                          err_flags)
     batch, T, ch = xbc.shape
     active = batch if active_batch is None else active_batch
-    ld = _tokens(xbc, "xbc", (batch, T), (ch,))
+    ld = _tokens(xbc, "xbc", (batch, T, ch), 2, ch)
     pool, cs, cc, ck, P = _conv_pool(conv_state, conv_strides, ch, width, xbc.dtype, P)
     ids, most = None, 0
     if accepted_node_ids is not None:
@@ -508,25 +525,25 @@ def ssu_conv_replay(xbc, conv_state, accepted_lengths, *, width, conv_strides,
          _vector(err_flags, "err_flags", 1))
 
 
-def _scan_args(lead, x, dt, A, B, C, state, out, D, z, dt_bias, state_indices, context_lengths,
+def _scan_args(x, dt, A, B, C, state, out, D, z, dt_bias, state_indices, context_lengths,
                err_flags, slot_stride, P):
     """The arguments scan_prefill and scan_decode share, up to state_indices."""
     dev = _common_device(x, dt, A, B, C, state, out, D, z, dt_bias, state_indices,
                          context_lengths, err_flags)
-    ch = x.shape[-1]
+    shape, xdt = x.shape, x.dtype
+    lead, ch = len(shape) - 1, shape[-1]
     G, N = B.shape[-2:]
-    if out is not None and (out.dtype != x.dtype or out.shape != x.shape or
-                            not out.is_contiguous()):
-        raise ValueError("out must be contiguous, in x's shape and dtype")
-    if z is not None and z.dtype != x.dtype:
+    per, bc = G * N, (*shape[:-1], G, N)
+    if z is not None and z.dtype is not xdt:
         raise ValueError("z must have x's dtype")
-    if C is not None and C.dtype != B.dtype:
+    if C is not None and C.dtype is not B.dtype:
         raise ValueError("C must have B's dtype")
     if state.dim() == 3:
-        if tuple(state.shape[1:]) != (ch, N) or state.stride(2) != 1 or state.stride(1) != N:
+        size, step = state.shape, state.stride()
+        if size[1:] != (ch, N) or step[1:] != (N, 1):
             raise ValueError(f"state must be [P, {ch}, {N}], contiguous inside a slot")
-        stride = state.stride(0) if slot_stride is None else slot_stride
-        P = state.shape[0] if P is None else P
+        stride = step[0] if slot_stride is None else slot_stride
+        P = size[0] if P is None else P
     else:
         if state.dim() != 1 or not state.is_contiguous():
             raise ValueError("state must be [P, channels, dstate] or flat contiguous storage")
@@ -534,17 +551,16 @@ def _scan_args(lead, x, dt, A, B, C, state, out, D, z, dt_bias, state_indices, c
         P = state.numel() // max(stride, 1) if P is None else P
     if P > 0 and (P - 1) * stride + ch * N > _extent(state):
         raise ValueError(f"state does not hold {P} slots of stride {stride}")
-    f32, inner = torch.float32, (ch,)
+    f32 = torch.float32
     return dev, G, N, P, [
-        x.data_ptr(), _dt(x, "x"), _tokens(x, "x", lead, inner), dt.data_ptr(), _dt(dt, "dt"),
-        _tokens(dt, "dt", lead, inner), _dense(A, "A", (ch, N), f32), B.data_ptr(),
-        None if C is None else C.data_ptr(), _dt(B, "B"), _tokens(B, "B", lead, (G, N)),
-        G * N if C is None else _tokens(C, "C", lead, (G, N)),
+        x.data_ptr(), _dt(x, "x"), _tokens(x, "x", shape, lead, ch), dt.data_ptr(), _dt(dt, "dt"),
+        _tokens(dt, "dt", shape, lead, ch), _dense(A, "A", (ch, N), f32), B.data_ptr(),
+        None if C is None else C.data_ptr(), _dt(B, "B"), _tokens(B, "B", bc, lead, per),
+        per if C is None else _tokens(C, "C", bc, lead, per),
         _vector(dt_bias, "dt_bias", ch, f32), _vector(D, "D", ch, f32),
-        None if z is None else z.data_ptr(), 0 if z is None else _tokens(z, "z", lead, inner),
-        state.data_ptr(), _dt(state, "state"), stride, P,
-        None if out is None else out.data_ptr(),
-        _vector(state_indices, "state_indices", lead[0])]
+        None if z is None else z.data_ptr(), 0 if z is None else _tokens(z, "z", shape, lead, ch),
+        state.data_ptr(), _dt(state, "state"), stride, P, _dense(out, "out", shape, xdt),
+        _vector(state_indices, "state_indices", shape[0])]
 
 
 def scan_prefill(x, dt, A, B, C, state, out, *, D=None, z=None, dt_bias=None, dt_softplus=True,
@@ -557,7 +573,7 @@ def scan_prefill(x, dt, A, B, C, state, out, *, D=None, z=None, dt_bias=None, dt
     ``out=None`` only advances it (C may then be None)."""
     batch, T, ch = x.shape
     active = batch if active_batch is None else active_batch
-    dev, G, N, P, args = _scan_args((batch, T), x, dt, A, B, C, state, out, D, z, dt_bias,
+    dev, G, N, P, args = _scan_args(x, dt, A, B, C, state, out, D, z, dt_bias,
                                     state_indices, context_lengths, err_flags, slot_stride, P)
     _debug_indices(state_indices, P, active, stream)
     _run("scan_prefill", dev, stream, *args, _vector(context_lengths, "context_lengths", batch),
@@ -573,7 +589,7 @@ def scan_decode(x, dt, A, B, C, state, out, *, D=None, z=None, dt_bias=None, dt_
     [batch, G, dstate]; other arguments as in scan_prefill; the state is updated in place."""
     batch, ch = x.shape
     active = batch if active_batch is None else active_batch
-    dev, G, N, P, args = _scan_args((batch,), x, dt, A, B, C, state, out, D, z, dt_bias,
+    dev, G, N, P, args = _scan_args(x, dt, A, B, C, state, out, D, z, dt_bias,
                                     state_indices, None, err_flags, slot_stride, P)
     _debug_indices(state_indices, P, active, stream)
     _run("scan_decode", dev, stream, *args, batch, active, ch, G, N, int(bool(dt_softplus)),
@@ -598,9 +614,9 @@ def spec_verify(tokens, target_probs, uniforms, uniform_sample, accepted_lengths
     active = batch if active_batch is None else active_batch
     ldq = 0
     if draft_probs is not None:
-        if draft_probs.dtype != target_probs.dtype:
+        if draft_probs.dtype is not target_probs.dtype:
             raise ValueError("draft_probs must have target_probs' dtype")
-        ldq = _tokens(draft_probs, "draft_probs", (batch, max(T - 1, 0)), (V,))
+        ldq = _tokens(draft_probs, "draft_probs", (batch, max(T - 1, 0), V), 2, V)
     i32, f32 = torch.int32, torch.float32
     most = 0
     if accepted_node_ids is not None:
@@ -610,7 +626,7 @@ def spec_verify(tokens, target_probs, uniforms, uniform_sample, accepted_lengths
     _run("spec_verify", dev, stream, _dense(tokens, "tokens", (batch, T), i32),
          target_probs.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(),
          _dt(target_probs, "target_probs"),
-         _tokens(target_probs, "target_probs", (batch, T), (V,)), ldq,
+         _tokens(target_probs, "target_probs", (batch, T, V), 2, V), ldq,
          _dense(uniforms, "uniforms", (batch, T), f32),
          _vector(uniform_sample, "uniform_sample", batch, f32),
          _vector(context_lengths, "context_lengths", batch),
