@@ -22,35 +22,76 @@ __device__ __forceinline__ float exp2_fast(float v)
     return r;
 }
 
-// log(1 + e^v) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1]. log1p by Gregory's series
-// log1p(e) = 2 (s + s^3/3 + s^5/5 + ...) with s = e / (2 + e) <= 1/3, cut where the next
-// term is below 2^-25 of the sum; it keeps full relative accuracy for the small steps
-// (e << 1) that a log of 1 + e would lose. exp(-|v|) = 2^(hi + lo) with the product's
-// rounding error carried in lo.
-__device__ __forceinline__ float softplus_scan(float v)
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ float rcp_fast(float v)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// log(1 + e^v) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1], for two values. With
+// s = e / (2 + e) <= 1/3, log1p(e) = 2 atanh(s) = 2 s (1 + s^2/3 + s^4/5 + ...), here with
+// the minimax polynomial of degree 4 in s^2 that starts with 1 (relative error 2^-27): it
+// keeps full relative accuracy for the small steps (e << 1) that a log of 1 + e would lose.
+// exp(-|v|) = 2^(hi + lo) with the product's rounding error carried in lo.
+__device__ __forceinline__ float2 softplus2(float2 v)
 {
     const float kLog2e = 1.44269504f, kLog2eLo = 1.92596e-8f, kLn2 = 0.693147181f;
-    const float a = fmaxf(-fabsf(v), -104.f);           // e^-104 is 0 in fp32
-    const float hi = a * kLog2e;
-    const float lo = fmaf(a, kLog2e, -hi) + a * kLog2eLo;
-    const float e = exp2_fast(hi) * fmaf(lo, kLn2, 1.f);
-    const float s = __fdividef(e, 2.f + e), q = s * s;
-    float p = 1.f / 13.f;
-    p = fmaf(p, q, 1.f / 11.f);
-    p = fmaf(p, q, 1.f / 9.f);
-    p = fmaf(p, q, 1.f / 7.f);
-    p = fmaf(p, q, 1.f / 5.f);
-    p = fmaf(p, q, 1.f / 3.f);
-    p = fmaf(p, q, 1.f);
-    return fmaf(2.f * s, p, v < 0.f ? 0.f : v);         // a NaN stays one
+    const float2 a = make_float2(fmaxf(-fabsf(v.x), -104.f),       // e^-104 is 0 in fp32
+                                 fmaxf(-fabsf(v.y), -104.f));
+    const float2 hi = mul2(a, both(kLog2e));
+    const float2 lo = fma2(a, both(kLog2eLo), fma2(a, both(kLog2e), make_float2(-hi.x, -hi.y)));
+    const float2 e = mul2(make_float2(exp2_fast(hi.x), exp2_fast(hi.y)),
+                          fma2(lo, both(kLn2), both(1.f)));
+    const float2 w = add2(e, both(2.f));
+    const float2 s = mul2(e, make_float2(rcp_fast(w.x), rcp_fast(w.y)));
+    const float2 q = mul2(s, s);
+    float2 p = fma2(q, both(0.1400598629f), both(0.1400090158f));
+    p = fma2(p, q, both(0.2001076341f));
+    p = fma2(p, q, both(0.3333320916f));
+    p = fma2(p, q, both(1.f));
+    return fma2(add2(s, s), p, make_float2(v.x < 0.f ? 0.f : v.x, v.y < 0.f ? 0.f : v.y));
+}
+
+__device__ __forceinline__ float softplus_scan(float v) { return softplus2(both(v)).x; }
+
+// 2^v for two values by a polynomial on the multiply-add pipe, for part of a warp's
+// exponentials when the special-function unit is what the rest waits for: v = n + f with
+// |f| <= 1/2 by adding and subtracting 1.5 * 2^23 (round to nearest, n left in the low
+// bits), 2^f by the minimax polynomial of degree 5 that starts with 1 (relative error
+// 2^-23.4), and a multiplication by 2^n. Below -126 the result is 2^-126 for 0, from 128 on
+// infinity; a NaN stays one.
+__device__ __forceinline__ float2 exp2_poly2(float2 v)
+{
+    const float kMagic = 12582912.f;
+    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(v.x));          // -126
+    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(v.y));
+    asm("min.NaN.f32 %0, %0, 0f43000000;" : "+f"(v.x));          // 128
+    asm("min.NaN.f32 %0, %0, 0f43000000;" : "+f"(v.y));
+    const float2 r = add2(v, both(kMagic));
+    const float2 n = add2(r, both(-kMagic));
+    const float2 f = add2(v, make_float2(-n.x, -n.y));
+    float2 p = fma2(f, both(0.001326472731f), both(0.009671512991f));
+    p = fma2(p, f, both(0.05550733581f));
+    p = fma2(p, f, both(0.2402224243f));
+    p = fma2(p, f, both(0.6931470037f));
+    p = fma2(p, f, both(1.f));
+    const float2 s = make_float2(__int_as_float((__float_as_int(r.x) << 23) + 0x3f800000),
+                                 __int_as_float((__float_as_int(r.y) << 23) + 0x3f800000));
+    return mul2(p, s);
 }
 
 // silu with the approximate exponential and division: relative error below 2^-20 for
 // |z| < 20, which a 16-bit output's rounding (2^-9 or 2^-11) hides; fp32 outputs take the
-// accurate one.
+// accurate one. (Far below zero the reciprocal of 2^127 and more is 0, and so is the gate.)
 __device__ __forceinline__ float gate(float z, int out_dtype)
 {
-    return out_dtype == SSU_F32 ? silu_f(z) : __fdividef(z, 1.f + __expf(-z));
+    return out_dtype == SSU_F32 ? silu_f(z) : z * rcp_fast(1.f + exp2_fast(-1.44269504f * z));
 }
 
 // kS consecutive states (4, or 8) of a channel, in the pool's type. The element offset is

@@ -147,6 +147,19 @@ def test_slices_of_wider_rows(wide, xdt):
     compare(c, o, pool, err, *w)
 
 
+@pytest.mark.parametrize("N", [8, 16, 128, 256])
+@pytest.mark.parametrize("T", [300, 1100])
+def test_long_rows_of_few_channels(T, N):
+    """Rows split over several CTAs: ragged, empty and shorter than one part."""
+    c = make(T, 10, T, 20, 1, N, BF16 if N == 16 else F32, slots=[2, 5, -1, 3, 9, 0, 1, 40, 7, 4])
+    lengths = torch.tensor([T, 0, 5, 1, 15, 17, 100, 3, T - 1, T // 2 + 3], dtype=torch.int32)
+    o, pool = check(c, lengths)
+    check(c, lengths, update=False)
+    check(c, lengths, out=False)
+    again, same, _ = run(c, lengths)
+    assert same_bits(again, o) and same_bits(same, pool)
+
+
 def test_options_padding_and_flags():
     c = make(2, 6, 9, 24, 1, 32, F32, slots=[3, -1, 99, 0, 5, 1], z=False, D=False, bias=False,
              positive=True)
