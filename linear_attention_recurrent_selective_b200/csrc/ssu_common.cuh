@@ -274,6 +274,9 @@ int launch_conv_prefill(const ConvPrefillArgs &a, int x_dtype, cudaStream_t s);
 int launch_conv_replay(const ConvPrefillArgs &a, int x_dtype, cudaStream_t s);
 int launch_scan_decode(const ScanArgs &a, cudaStream_t s);
 int launch_scan_prefill(ScanArgs a, cudaStream_t s);
+int launch_scan_prefill_bf16(const ScanArgs &a, cudaStream_t s);
+int launch_scan_prefill_f16(const ScanArgs &a, cudaStream_t s);
+int launch_scan_prefill_f32(const ScanArgs &a, cudaStream_t s);
 int launch_verify(const VerifyArgs &a, int p_dtype, cudaStream_t s);
 int launch_gdn_decode(const GdnArgs &a, cudaStream_t s);
 int launch_clear(void *pool, int64_t bytes, cudaStream_t s);

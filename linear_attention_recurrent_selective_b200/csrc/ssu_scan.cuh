@@ -94,6 +94,15 @@ __device__ __forceinline__ float gate(float z, int out_dtype)
     return out_dtype == SSU_F32 ? silu_f(z) : z * rcp_fast(1.f + exp2_fast(-1.44269504f * z));
 }
 
+__device__ __forceinline__ float2 gate2(float2 z, int out_dtype)
+{
+    if (out_dtype == SSU_F32)
+        return make_float2(silu_f(z.x), silu_f(z.y));
+    const float2 m = mul2(z, both(-1.44269504f));
+    const float2 e = add2(make_float2(exp2_fast(m.x), exp2_fast(m.y)), both(1.f));
+    return mul2(z, make_float2(rcp_fast(e.x), rcp_fast(e.y)));
+}
+
 // kS consecutive states (4, or 8) of a channel, in the pool's type. The element offset is
 // a multiple of 4, so that every access is aligned to its size.
 template <int kS>

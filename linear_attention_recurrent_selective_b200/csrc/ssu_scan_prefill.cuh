@@ -1,0 +1,684 @@
+// ssu_scan_prefill.cuh -- the per-channel selective scan over the tokens of a prompt.
+//
+// The recurrence of ssu_scan_decode.cu run over t < L_b with the state held in registers:
+//     h[d,n] = exp(dt[t,d] A[d,n]) h[d,n] + dt[t,d] x[t,d] B[t,n]
+//     out[t,d] = (sum_n h[d,n] C[t,n] + D[d] x[t,d]) * silu(z[t,d])
+// The decay differs for every (channel, state), so there is no product of matrices in it:
+// N exponentials and 4 N multiply-adds per (token, channel).
+//
+// Bound: the special-function unit (16 exponentials a clock and SM, so one clock per
+// (token, channel) and SM at N = 16), ahead of memory (x, dt, z, out: 8 bytes).
+//
+// Layout: a lane holds 8 states of a channel, kL = N / 8 lanes a channel; a CTA takes a block
+// of neighbouring channels of one row and walks its tokens in chunks of kTok, whose raw
+// inputs arrive in shared memory by cp.async one chunk ahead (plain loads where rows are not
+// 16-byte aligned), with B and C widened to fp32 beside them: one barrier a chunk. A warp runs
+// its channels four tokens at a time. The lanes of a channel share out the four tokens: a
+// lane forms the steps dt and dt*x of its own (packed in pairs), hands them to the others by
+// shuffles, gets back the sums over all states of its own tokens from a transposing
+// butterfly, and finishes and stores their outputs. The next group's steps are formed while
+// this one runs. Rows run longest first.
+//
+// Few rows leave most of the card idle, so a long row may be split over a cluster of CTAs,
+// each taking a segment of its tokens. The recurrence is linear in the state: a segment
+// started from zero ends in h0, and started from h in exp(A sum dt) h + h0. So every CTA
+// but the first runs its segment from zero without outputs (about 2/3 of the work), the
+// ends are exchanged through distributed shared memory, each CTA folds those before it into
+// its true start, and runs its segment again with outputs. The first CTA starts from the
+// true state and runs once; its segment is 2/3 as long, so that the CTAs meet in time.
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include "ssu_scan.cuh"
+
+namespace ssu {
+namespace {
+
+using namespace scan;
+namespace cg = cooperative_groups;
+
+constexpr int kStates = 8;            // of a lane
+constexpr int kMinWarps = 16;         // of an SM: at most 128 registers a thread
+constexpr int kFill = 592;            // CTAs that give 148 SMs four each
+constexpr int kMaxParts = 16;         // CTAs of a cluster (above 8 by opt-in)
+
+// CH: neighbouring channels of a lane, 1 or 2.
+template <int N, int CH> struct Tile {
+    static constexpr int kL = N / kStates;                              // lanes of a channel
+    static constexpr int kWarps = N == 256 ? 8 / CH : (N >= 32 ? 4 : 4 / CH);
+    static constexpr int kThreads = 32 * kWarps;
+    // channels of a CTA: a multiple of 8, so that a row of them is whole 16-byte units
+    static constexpr int kCh = kThreads / kL * CH;
+    static constexpr int kTok = N <= 64 ? 32 : (N == 128 ? 16 : 8);     // tokens of a chunk
+    static constexpr int kOwn = kL >= 4 ? 1 : 4 / kL;                   // tokens of a lane, of 4
+    // the lane's values of a group as packed pairs: of its two channels, or of two tokens
+    static constexpr int kPr = CH == 2 ? kOwn : (kOwn + 1) / 2;
+    // shared memory: B and C widened, two stages of [2][kTok][N]; two stages of raw x, dt, z,
+    // B, C; where rows are split, the segment's end state [kCh][N] and sum of steps [kCh]
+    static constexpr int kWide = 2 * kTok * N * 4;
+    static constexpr int kFixed = 2 * kWide;
+    static constexpr int kEnds = kCh * N * 4 + kCh * 4;
+    static_assert(kCh % 8 == 0, "");
+};
+
+__host__ __device__ __forceinline__ int esize(int dtype) { return dtype == SSU_F32 ? 4 : 2; }
+
+// Byte offsets of the raw inputs of one chunk.
+struct Raw {
+    int x, dt, z, B, C, bytes;
+};
+
+template <int N, int CH>
+__host__ __device__ __forceinline__ Raw raw_layout(int ex, int ed, int eb, bool z)
+{
+    using T = Tile<N, CH>;
+    Raw r;
+    r.x = 0;
+    r.dt = T::kTok * T::kCh * ex;
+    r.z = r.dt + T::kTok * T::kCh * ed;
+    r.B = r.z + (z ? T::kTok * T::kCh * ex : 0);
+    r.C = r.B + T::kTok * N * eb;
+    r.bytes = r.C + T::kTok * N * eb;
+    return r;
+}
+
+__device__ __forceinline__ void copy16(void *dst, const void *src, int bytes)
+{
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes)
+                 : "memory");
+}
+
+constexpr int log2_of(int n) { return n <= 1 ? 0 : 1 + log2_of(n / 2); }
+
+// Bring kTok rows of kRow (a power of two) elements (of which the first `left` exist) of tokens t0.. into
+// shared memory, zeros beyond token t1 and element `left`. Row t starts at element
+// t * ld of src.
+template <int kThreads, int kTok, int kRow>
+__device__ __forceinline__ void fetch_rows(uint8_t *dst, const void *src, int es, int64_t ld,
+                                           int left, int t0, int t1, bool vec, int tid)
+{
+    const char *const p = static_cast<const char *>(src);
+    if (vec) {
+        const int lg = es == 4 ? 2 : 3, lp = log2_of(kRow) - lg;        // 2^lp units of a row
+        for (int u = tid; u < kTok << lp; u += kThreads) {
+            const int t = u >> lp, e = (u & ((1 << lp) - 1)) << lg;
+            const int n = t0 + t < t1 ? min(max(left - e, 0), 1 << lg) * es : 0;
+            copy16(dst + u * 16, n ? p + ((t0 + t) * ld + e) * es : p, n);
+        }
+    } else {
+        for (int u = tid; u < kTok * kRow; u += kThreads) {
+            const int t = u / kRow, e = u % kRow;
+            const bool in = t0 + t < t1 && e < left;
+            if (es == 4)
+                reinterpret_cast<uint32_t *>(dst)[u] =
+                    in ? reinterpret_cast<const uint32_t *>(p)[(t0 + t) * ld + e] : 0u;
+            else
+                reinterpret_cast<uint16_t *>(dst)[u] =
+                    in ? reinterpret_cast<const uint16_t *>(p)[(t0 + t) * ld + e] : (uint16_t)0;
+        }
+    }
+}
+
+// Element i of a raw array in shared memory.
+__device__ __forceinline__ float elem_at(const uint8_t *raw, int dtype, int i)
+{
+    if (dtype == SSU_F32)
+        return reinterpret_cast<const float *>(raw)[i];
+    if (dtype == SSU_F16)
+        return __half2float(reinterpret_cast<const __half *>(raw)[i]);
+    return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(raw)[i]);
+}
+
+// Elements i and j of a raw array (i even and j = i + 1 where kAdjacent).
+template <bool kAdjacent>
+__device__ __forceinline__ float2 elems_at(const uint8_t *raw, int dtype, int i, int j)
+{
+    if constexpr (kAdjacent) {
+        if (dtype == SSU_F32)
+            return reinterpret_cast<const float2 *>(raw)[i >> 1];
+        if (dtype == SSU_F16)
+            return __half22float2(reinterpret_cast<const __half2 *>(raw)[i >> 1]);
+        return __bfloat1622float2(reinterpret_cast<const __nv_bfloat162 *>(raw)[i >> 1]);
+    } else {
+        const float v = elem_at(raw, dtype, i);
+        return make_float2(v, i == j ? v : elem_at(raw, dtype, j));
+    }
+}
+
+// Outputs of two neighbouring channels, as one access where `vec` (both exist and the pair
+// is aligned).
+__device__ __forceinline__ void store_pair(void *p, int dtype, int64_t at, bool two, bool vec,
+                                           float2 o)
+{
+    if (vec && two) {
+        if (dtype == SSU_F32)
+            *reinterpret_cast<float2 *>(static_cast<float *>(p) + at) = o;
+        else if (dtype == SSU_F16)
+            *reinterpret_cast<__half2 *>(static_cast<__half *>(p) + at) =
+                __floats2half2_rn(o.x, o.y);
+        else
+            *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p) + at) =
+                __floats2bfloat162_rn(o.x, o.y);
+    } else {
+        st_f32(p, dtype, at, o.x);
+        if (two)
+            st_f32(p, dtype, at + 1, o.y);
+    }
+}
+
+// Widen kAll raw elements to fp32; a thread takes what it brought by fetch_rows, so that it
+// needs to wait for its own copies only.
+template <int kThreads, int kAll>
+__device__ __forceinline__ void widen_rows(float *dst, const uint8_t *raw, int dtype, bool vec,
+                                           int tid)
+{
+    if (!vec) {
+        for (int u = tid; u < kAll; u += kThreads)
+            dst[u] = elem_at(raw, dtype, u);
+    } else if (dtype == SSU_F32) {
+        for (int u = tid; u < kAll / 4; u += kThreads)
+            reinterpret_cast<uint4 *>(dst)[u] = reinterpret_cast<const uint4 *>(raw)[u];
+    } else {
+        for (int u = tid; u < kAll / 8; u += kThreads) {
+            float f[8];
+            if (dtype == SSU_F16)
+                Vec16<__half>::unpack(reinterpret_cast<const uint4 *>(raw)[u], f);
+            else
+                Vec16<__nv_bfloat16>::unpack(reinterpret_cast<const uint4 *>(raw)[u], f);
+            reinterpret_cast<uint4 *>(dst)[2 * u] = Vec16<float>::pack(f);
+            reinterpret_cast<uint4 *>(dst)[2 * u + 1] = Vec16<float>::pack(f + 4);
+        }
+    }
+}
+
+// Of four tokens, the i-th that lane ln of a channel owns (lanes beyond the fourth repeat).
+template <int kL> __device__ __forceinline__ int own(int ln, int i)
+{
+    return kL == 1 ? i : kL == 2 ? ln + 2 * i : ln & 3;
+}
+
+// Value of token u (of four) and channel c from the lane that owns it; v: this lane's own.
+template <int kL, int CH, int kPr>
+__device__ __forceinline__ float of_token(const float2 (&v)[kPr], int u, int c)
+{
+    const int i = kL == 1 ? u : kL == 2 ? u >> 1 : 0;       // its index at the owner
+    const float w = CH == 2 ? (c ? v[i].y : v[i].x) : (i & 1 ? v[i >> 1].y : v[i >> 1].x);
+    return kL == 1 ? w : __shfl_sync(~0u, w, kL == 2 ? u & 1 : u, kL);
+}
+
+// Sums over the lanes of a channel of four values (four tokens) of CH channels: each lane
+// gets those of its own tokens. At each of the first two steps a lane hands half of its
+// values to its partner.
+template <int kL, int CH, int kPr>
+__device__ __forceinline__ void sum_own(const float (&v)[CH][4], float2 (&s)[kPr], int ln)
+{
+    float own[CH][4];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        if constexpr (kL == 1) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                own[c][u] = v[c][u];
+        } else {
+            const bool hi = ln & 1;                         // odd tokens
+            const float g0 = __shfl_xor_sync(~0u, hi ? v[c][0] : v[c][1], 1);
+            const float g1 = __shfl_xor_sync(~0u, hi ? v[c][2] : v[c][3], 1);
+            own[c][0] = (hi ? v[c][1] : v[c][0]) + g0;
+            own[c][1] = (hi ? v[c][3] : v[c][2]) + g1;
+            if constexpr (kL >= 4) {
+                const bool h2 = ln & 2;                     // tokens 2, 3
+                const float g = __shfl_xor_sync(~0u, h2 ? own[c][0] : own[c][1], 2);
+                own[c][0] = (h2 ? own[c][1] : own[c][0]) + g;
+#pragma unroll
+                for (int o = 4; o < kL; o <<= 1)
+                    own[c][0] += __shfl_xor_sync(~0u, own[c][0], o);
+            }
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < kPr; ++p)
+        s[p] = CH == 2 ? make_float2(own[0][p], own[CH - 1][p])
+                       : make_float2(own[0][2 * p], own[0][kL >= 4 ? 0 : 2 * p + 1]);
+}
+
+// Length used to order the rows: padding and out-of-range rows do (almost) no work.
+__device__ __forceinline__ int sched_len(const ScanArgs &a, int b)
+{
+    const int slot = a.idx ? a.idx[b] : b;
+    if (slot < 0 || slot >= a.P)
+        return 0;
+    const int L = a.ctx ? a.ctx[b] : a.T;
+    return L < 0 ? 0 : (L > a.T ? a.T : L);
+}
+
+// The row of rank `rank` by decreasing length (ties by index), for up to kRankMax rows.
+__device__ __forceinline__ int ranked_row(const ScanArgs &a, int rank, int *s_len, int *s_row)
+{
+    if (!a.ctx || a.active > kRankMax)
+        return rank;
+    const int tid = threadIdx.x;
+    if (tid < a.active)
+        s_len[tid] = sched_len(a, tid);
+    __syncthreads();
+    if (tid < a.active) {
+        const int mine = s_len[tid];
+        int r = 0;
+        for (int o = 0; o < a.active; ++o)
+            r += (s_len[o] > mine) || (s_len[o] == mine && o < tid);
+        if (r == rank)
+            *s_row = tid;
+    }
+    __syncthreads();
+    return *s_row;
+}
+
+// What a lane keeps of its channels: states and decay rates as pairs of neighbours.
+template <int CH> struct Lane {
+    float2 h[CH][kStates / 2], rate[CH][kStates / 2];
+    float sum[CH];                              // steps since the segment's start
+};
+
+// The CTA's block of channels: all of one group.
+struct Block {
+    int g, d0, n;                               // group, first channel, channels
+};
+
+// Run tokens [t_begin, t_end) of the row through the lane's states; kOut: form the outputs.
+// DT: the type of x, dt, z, B and C where they share it and it was compiled in, else -1.
+template <int N, int CH, int DT, bool kOut>
+__device__ __forceinline__ void run_tokens(const ScanArgs &a, Lane<CH> &st, uint8_t *smem, int b,
+                                           const Block blk, int t_begin, int t_end)
+{
+    using T = Tile<N, CH>;
+    constexpr int kL = T::kL, kTok = T::kTok, kCh = T::kCh, kOwn = T::kOwn, kPr = T::kPr;
+    constexpr int kP = kStates / 2, kThreads = T::kThreads;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int ln = lane % kL, n0 = ln * kStates, ch = tid / kL * CH;
+    const int64_t row = (int64_t)b * a.T;
+
+    // rows of this CTA's channels, from token 0 of the row
+    const int xt = DT < 0 ? a.x_dtype : DT, dtt = DT < 0 ? a.dt_dtype : DT;
+    const int bct = DT < 0 ? a.bc_dtype : DT;
+    const int ex = esize(xt), ed = esize(dtt), eb = esize(bct);
+    const bool gated = kOut && a.z, softplus = a.softplus;
+    const Raw lay = raw_layout<N, CH>(ex, ed, eb, a.z);
+    uint8_t *const raw0 = smem + T::kFixed;
+    const char *const gx = static_cast<const char *>(a.x) + (row * a.ldx + blk.d0) * ex;
+    const char *const gd = static_cast<const char *>(a.dt) + (row * a.lddt + blk.d0) * ed;
+    const char *const gz = static_cast<const char *>(a.z) + (row * a.ldz + blk.d0) * ex;
+    const char *const gB = static_cast<const char *>(a.B) + (row * a.ldb + (int64_t)blk.g * N) * eb;
+    const char *const gC = static_cast<const char *>(a.C) + (row * a.ldc + (int64_t)blk.g * N) * eb;
+
+    // the lane's channels and, in pairs, its own values of a group: the tokens at 2 p and
+    // 2 p + 1 of its list of one channel, or token p of both channels
+    const bool live = ch < blk.n, live1 = CH == 2 ? ch + 1 < blk.n : live;
+    const int d = blk.d0 + ch;
+    float2 bias = make_float2(0.f, 0.f), skip = bias;
+    if (a.dt_bias) {
+        bias.x = live ? a.dt_bias[d] : 0.f;
+        bias.y = CH == 1 ? bias.x : live1 ? a.dt_bias[d + 1] : 0.f;
+    }
+    if (kOut && a.Dp) {
+        skip.x = live ? a.Dp[d] : 0.f;
+        skip.y = CH == 1 ? skip.x : live1 ? a.Dp[d + 1] : 0.f;
+    }
+    const auto first_of = [&](int p) { return own<kL>(ln, CH == 2 ? p : 2 * p); };
+    const auto second_of = [&](int p) {
+        return CH == 2 ? own<kL>(ln, p) : own<kL>(ln, kOwn > 1 ? 2 * p + 1 : 0);
+    };
+
+    // (Options are taken by selection: a branch would keep the four stages of a group --
+    // steps of the next, scan, sums, outputs -- from being interleaved.)
+    // one round ahead of the first chunk only fetches it
+    int stage = 1;
+    for (int t0 = t_begin - kTok; t0 < t_end; t0 += kTok, stage ^= 1) {
+        const uint8_t *const r = raw0 + stage * lay.bytes;
+        float *const s_B = reinterpret_cast<float *>(smem + stage * T::kWide);
+        float *const s_C = s_B + kTok * N;
+        if (t0 >= t_begin) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            widen_rows<kThreads, kTok * N>(s_B, r + lay.B, bct, a.vec & 16, tid);
+            if (kOut)
+                widen_rows<kThreads, kTok * N>(s_C, r + lay.C, bct, a.vec & 32, tid);
+            __syncthreads();            // the chunk is here, the other stage is free
+        }
+        if (const int t1 = t0 + kTok; t1 < t_end) {
+            uint8_t *const to = raw0 + (stage ^ 1) * lay.bytes;
+            fetch_rows<kThreads, kTok, kCh>(to + lay.x, gx, ex, a.ldx, blk.n, t1, t_end, a.vec & 1,
+                                            tid);
+            fetch_rows<kThreads, kTok, kCh>(to + lay.dt, gd, ed, a.lddt, blk.n, t1, t_end,
+                                            a.vec & 2, tid);
+            fetch_rows<kThreads, kTok, N>(to + lay.B, gB, eb, a.ldb, N, t1, t_end, a.vec & 16, tid);
+            if (gated)
+                fetch_rows<kThreads, kTok, kCh>(to + lay.z, gz, ex, a.ldz, blk.n, t1, t_end,
+                                                a.vec & 4, tid);
+            if (kOut)
+                fetch_rows<kThreads, kTok, N>(to + lay.C, gC, eb, a.ldc, N, t1, t_end, a.vec & 32,
+                                              tid);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        if (t0 < t_begin)
+            continue;
+        // the lane's own tokens of the group at t: inputs and steps; none beyond the end
+        const auto steps = [&](int t, float2 (&x)[kPr], float2 (&dt)[kPr], float2 (&dx)[kPr]) {
+#pragma unroll
+            for (int p = 0; p < kPr; ++p) {
+                const int ta = t + first_of(p), tb = t + second_of(p);
+                const int ia = ta * kCh + ch, ib = tb * kCh + ch + CH - 1;
+                x[p] = elems_at<CH == 2>(r + lay.x, xt, ia, ib);
+                dt[p] = add2(elems_at<CH == 2>(r + lay.dt, dtt, ia, ib), bias);
+                const float2 sp = softplus2(dt[p]);
+                dt[p].x = softplus ? sp.x : dt[p].x;
+                dt[p].y = softplus ? sp.y : dt[p].y;
+                dt[p].x = t0 + ta < t_end ? dt[p].x : 0.f;
+                dt[p].y = t0 + tb < t_end ? dt[p].y : 0.f;
+                dx[p] = mul2(dt[p], x[p]);
+            }
+        };
+        float2 x[kPr], dt[kPr], dx[kPr];
+        steps(0, x, dt, dx);
+
+#pragma unroll 1
+        for (int t = 0; t < kTok; t += 4) {
+            float y[CH][4];
+            float2 xn[kPr], dtn[kPr], dxn[kPr];
+            steps((t + 4) & (kTok - 1), xn, dtn, dxn);      // (the last one's are not used)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float2 Bv[kP], Cv[kP];
+#pragma unroll
+                for (int i = 0; i < kP; i += 2) {
+                    const float4 v = *reinterpret_cast<const float4 *>(s_B + (t + u) * N + n0 + 2 * i);
+                    Bv[i] = make_float2(v.x, v.y);
+                    Bv[i + 1] = make_float2(v.z, v.w);
+                    if (kOut) {
+                        const float4 w =
+                            *reinterpret_cast<const float4 *>(s_C + (t + u) * N + n0 + 2 * i);
+                        Cv[i] = make_float2(w.x, w.y);
+                        Cv[i + 1] = make_float2(w.z, w.w);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    const float2 d2 = both(of_token<kL, CH, kPr>(dt, u, c));
+                    const float2 x2 = both(of_token<kL, CH, kPr>(dx, u, c));
+                    float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < kP; ++i) {
+                        const float2 v = mul2(d2, st.rate[c][i]);
+                        const float2 e = make_float2(exp2_fast(v.x), exp2_fast(v.y));
+                        st.h[c][i] = fma2(st.h[c][i], e, mul2(x2, Bv[i]));
+                        if (kOut)
+                            acc = i ? fma2(st.h[c][i], Cv[i], acc) : mul2(st.h[c][i], Cv[i]);
+                    }
+                    if (kOut)
+                        y[c][u] = acc.x + acc.y;
+                    else
+                        st.sum[c] += d2.x;
+                }
+            }
+            if (kOut) {
+                float2 o[kPr];
+                sum_own<kL, CH, kPr>(y, o, ln);
+#pragma unroll
+                for (int p = 0; p < kPr; ++p) {
+                    const int ta = t + first_of(p), tb = t + second_of(p);
+                    o[p] = fma2(skip, x[p], o[p]);
+                    // (without a gate this reads other inputs and drops the product)
+                    const float2 z = elems_at<CH == 2>(r + lay.z, xt, ta * kCh + ch,
+                                                       tb * kCh + ch + CH - 1);
+                    const float2 go = mul2(o[p], gate2(z, xt));
+                    o[p].x = gated ? go.x : o[p].x;
+                    o[p].y = gated ? go.y : o[p].y;
+                    if (live && (kL <= 4 || ln < 4) && t0 + ta < t_end) {
+                        const int64_t at = (row + t0 + ta) * a.D + d;
+                        if constexpr (CH == 2) {
+                            store_pair(a.out, xt, at, live1, a.vec & 8, o[p]);
+                        } else {
+                            st_f32(a.out, xt, at, o[p].x);
+                            if (kOwn > 1 && t0 + tb < t_end)
+                                st_f32(a.out, xt, at + (int64_t)(tb - ta) * a.D, o[p].y);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int p = 0; p < kPr; ++p) {
+                x[p] = xn[p];
+                dt[p] = dtn[p];
+                dx[p] = dxn[p];
+            }
+        }
+    }
+}
+
+template <int N, int CH, int DT>
+__global__ void __launch_bounds__(Tile<N, CH>::kThreads, kMinWarps / Tile<N, CH>::kWarps)
+scan_prefill_kernel(const __grid_constant__ ScanArgs a, const int blocks, const int parts)
+{
+    using T = Tile<N, CH>;
+    constexpr int S = kStates, kP = S / 2, kL = T::kL, kCh = T::kCh, kThreads = T::kThreads;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int s_len[kRankMax], s_row;
+
+    const int tid = threadIdx.x;
+    const int part = blockIdx.x % parts, unit = blockIdx.x / parts;
+    const int b = ranked_row(a, unit / blocks, s_len, &s_row);
+    const int per = a.D / a.G, of_group = blocks / a.G;     // channels, blocks of a group
+    Block blk;
+    blk.g = unit % blocks / of_group;
+    blk.d0 = blk.g * per + unit % blocks % of_group * kCh;
+    blk.n = min(kCh, (blk.g + 1) * per - blk.d0);
+    const int slot = a.idx ? a.idx[b] : b;
+    const bool first = unit % blocks == 0 && part == 0 && tid == 0;
+    if (slot >= a.P) {                                      // caller bug: skip and report
+        if (first && a.err)
+            atomicOr(a.err, SSU_FLAG_INDEX_RANGE);
+        return;
+    }
+    if (slot < 0) {                                         // padding row: zeros
+        if (a.out && part == 0) {
+            for (int64_t v = tid; v < (int64_t)a.T * kCh; v += kThreads)
+                if (v % kCh < blk.n)
+                    st_f32(a.out, a.x_dtype, ((int64_t)b * a.T + v / kCh) * a.D + blk.d0 + v % kCh,
+                           0.f);
+        }
+        return;
+    }
+    int L = a.T;
+    if (a.ctx) {
+        L = a.ctx[b];
+        if (first && a.err && (L < 0 || L > a.T))
+            atomicOr(a.err, L < 0 ? SSU_FLAG_NEGATIVE_LENGTH : SSU_FLAG_CONTEXT_RANGE);
+        L = L < 0 ? 0 : (L > a.T ? a.T : L);
+    }
+    if (L == 0)
+        return;
+
+    // the lane's states and decay rates
+    const int ln = tid % kL, n0 = ln * S, ch = tid / kL * CH;
+    const int64_t pool0 = (int64_t)slot * a.slot_stride;
+    Lane<CH> s;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int64_t at = ((int64_t)blk.d0 + min(ch + c, blk.n - 1)) * N + n0;
+        float h[S] = {}, rate[S];
+        load_decay_rates<S>(a.A, at, rate);
+        if (part == 0)
+            load_states<S>(a.state, a.state_dtype, pool0 + at, h);
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+            s.h[c][i] = make_float2(h[2 * i], h[2 * i + 1]);
+            s.rate[c][i] = make_float2(rate[2 * i], rate[2 * i + 1]);
+        }
+        s.sum[c] = 0.f;
+    }
+
+    // this CTA's tokens: segments in units of a chunk, the first 2 shares, the others 3
+    cg::cluster_group cluster = cg::this_cluster();
+    const int chunks = (L + T::kTok - 1) / T::kTok, shares = 3 * parts - 1;
+    const auto bound = [&](int p) {
+        return p == 0 ? 0 : min((int)((int64_t)chunks * (3 * p - 1) / shares) * T::kTok, L);
+    };
+    const int t0 = bound(part), t1 = part + 1 == parts ? L : bound(part + 1);
+    const bool last = part + 1 == parts;
+    const Raw lay = raw_layout<N, CH>(esize(a.x_dtype), esize(a.dt_dtype), esize(a.bc_dtype), a.z);
+    float *const s_end = reinterpret_cast<float *>(smem + T::kFixed + 2 * lay.bytes);
+    float *const s_sum = s_end + kCh * N;
+#pragma unroll 1
+    for (int pass = part > 0 && last ? 1 : 0; pass < (part ? 2 : 1); ++pass) {
+        if (pass == 1) {
+            // every end is there: fold those before this segment into its start
+            cluster.sync();
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                for (int q = 0; q < part; ++q) {
+                    const float *const end = cluster.map_shared_rank(s_end, q) + (ch + c) * N + n0;
+                    const float sum = q ? *cluster.map_shared_rank(s_sum + ch + c, q) : 0.f;
+#pragma unroll
+                    for (int i = 0; i < kP; ++i) {
+                        const float2 e = *reinterpret_cast<const float2 *>(end + 2 * i);
+                        const float2 f = make_float2(exp2_fast(sum * s.rate[c][i].x),
+                                                     exp2_fast(sum * s.rate[c][i].y));
+                        s.h[c][i] = q ? fma2(s.h[c][i], f, e) : e;
+                    }
+                }
+            }
+            cluster.barrier_arrive();           // the others' ends are read
+        }
+        if (a.out && (pass == 1 || part == 0))
+            run_tokens<N, CH, DT, true>(a, s, smem, b, blk, t0, t1);
+        else if (pass == 0 || last)
+            run_tokens<N, CH, DT, false>(a, s, smem, b, blk, t0, t1);
+        if (pass == 0 && parts > 1) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+#pragma unroll
+                for (int i = 0; i < kP; ++i)
+                    *reinterpret_cast<float2 *>(s_end + (ch + c) * N + n0 + 2 * i) = s.h[c][i];
+                if (ln == 0)
+                    s_sum[ch + c] = s.sum[c];
+            }
+        }
+    }
+    if (parts > 1) {
+        if (part == 0) {
+            cluster.sync();
+            cluster.barrier_arrive();
+        }
+        cluster.barrier_wait();                 // no CTA leaves while its end may be read
+    }
+
+    if (a.update && last) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+            if (ch + c < blk.n) {
+                float h[S];
+#pragma unroll
+                for (int i = 0; i < kP; ++i) {
+                    h[2 * i] = s.h[c][i].x;
+                    h[2 * i + 1] = s.h[c][i].y;
+                }
+                store_states<S>(a.state, a.state_dtype,
+                                pool0 + ((int64_t)blk.d0 + ch + c) * N + n0, h);
+            }
+    }
+}
+
+// Rows are split into p parts while the CTAs fill less than half of the card's room for them
+// and every part keeps at least 64 tokens: that costs (3 p + 2) / (3 p - 1) of a row's work
+// and runs it p times as wide, so two parts gain nothing.
+int parts_of(int64_t units, int T)
+{
+    int p = 1;
+    while (p < kMaxParts && units * p * 2 <= kFill && T >= 128 * p)
+        p *= 2;
+    return p < 4 ? 1 : p;
+}
+
+// Clusters of more than 8 CTAs need the kernel's consent, given once per device.
+template <auto kernel> bool wide_clusters()
+{
+    static std::once_flag once[kMaxDevices];
+    static bool ok[kMaxDevices];
+    const int dev = current_device();
+    if (dev < 0)
+        return false;
+    std::call_once(once[dev], [&] {
+        ok[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+                  cudaSuccess;
+    });
+    return ok[dev];
+}
+
+template <int N, int CH> int64_t blocks_of(const ScanArgs &a)
+{
+    constexpr int kCh = Tile<N, CH>::kCh;
+    return (int64_t)a.G * ((a.D / a.G + kCh - 1) / kCh);
+}
+
+template <int N, int CH, int DT> int launch_c(const ScanArgs &a, cudaStream_t s)
+{
+    using T = Tile<N, CH>;
+    const int64_t blocks = blocks_of<N, CH>(a), units = blocks * a.active;
+    const int parts = parts_of(units, a.T);
+    const int64_t grid = units * parts;
+    if (blocks > 0x7fffffffLL || grid > 0x7fffffffLL)
+        return SSU_ERR_SHAPE;
+    const Raw lay = raw_layout<N, CH>(esize(a.x_dtype), esize(a.dt_dtype), esize(a.bc_dtype), a.z);
+    // the largest layout (fp32 inputs) sets the kernel's shared-memory limit
+    constexpr int kMost =
+        T::kFixed + 2 * (T::kTok * T::kCh * 12 + T::kTok * N * 8) + T::kEnds;
+    const KernelFacts *f = kernel_facts<scan_prefill_kernel<N, CH, DT>>(T::kThreads, kMost);
+    if (!f || f->status != SSU_OK)
+        return SSU_ERR_CUDA;
+    if (parts > 8 && !wide_clusters<scan_prefill_kernel<N, CH, DT>>())
+        return SSU_ERR_CUDA;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = parts;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(T::kThreads);
+    cfg.dynamicSmemBytes = T::kFixed + 2 * lay.bytes + (parts > 1 ? T::kEnds : 0);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = parts > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, scan_prefill_kernel<N, CH, DT>, a, (int)blocks, parts) ==
+                   cudaSuccess
+               ? SSU_OK
+               : SSU_ERR_CUDA;
+}
+
+// Two channels a lane halve the exchanges between lanes and the reads of B and C, at twice
+// the registers: better from 64 states on (8 lanes a channel), where that leaves every SM
+// eight warps; one channel a lane is better below.
+template <int N, int DT> int launch_n(const ScanArgs &a, cudaStream_t s)
+{
+    if constexpr (N >= 64) {
+        const int64_t warps = blocks_of<N, 2>(a) * Tile<N, 2>::kWarps * a.active;
+        if (warps >= 1184)
+            return launch_c<N, 2, DT>(a, s);
+    }
+    return launch_c<N, 1, DT>(a, s);
+}
+
+template <int DT> int launch_dt(const ScanArgs &a, cudaStream_t s)
+{
+    switch (a.N) {
+    case 8: return launch_n<8, DT>(a, s);
+    case 16: return launch_n<16, DT>(a, s);
+    case 32: return launch_n<32, DT>(a, s);
+    case 64: return launch_n<64, DT>(a, s);
+    case 128: return launch_n<128, DT>(a, s);
+    case 256: return launch_n<256, DT>(a, s);
+    default: return SSU_ERR_UNSUPPORTED;
+    }
+}
+
+}  // namespace
+}  // namespace ssu
