@@ -268,8 +268,8 @@ int ssu_conv_decode(const void *xbc, int x_dtype, const void *conv_weight,
  *   update_state != 0: the window becomes the last width-1 of (window, the row's L_b
  *                tokens); 0: the pool is only read (verification: the accepted tokens enter
  *                by ssu_conv_replay)
- *   tree_parent_ids [batch, T] int32 (optional, as in ssu_ddtree; needs update_state == 0):
- *                the inputs before node t are its ancestors (parent, grandparent, ...), then
+ *   tree_parent_ids [batch, T] int32 (optional, as in ssu_ddtree, T <= 128; needs
+ *                update_state == 0): the inputs before node t are its ancestors (parent, grandparent, ...), then
  *                the window. A node with a parent outside [-1, L_b) among its width-1
  *                nearest ancestors gets outputs 0 and SSU_FLAG_TREE.
  *   width 1..16. Padding rows write zeros to the outputs at every t < T.

@@ -389,7 +389,8 @@ int ssu_conv_prefill(const void *xbc, int x_dtype, int64_t xbc_stride, const voi
         return rc;
     if (!state_indices && active_batch > P)
         return SSU_ERR_SHAPE;
-    if (tree_parent_ids && update_state)      // a tree's tokens enter by ssu_conv_replay
+    // a tree has at most 128 nodes, and its tokens enter the windows by ssu_conv_replay
+    if (tree_parent_ids && (update_state || T > 128))
         return SSU_ERR_SHAPE;
     if (active_batch == 0 || T == 0)
         return SSU_OK;

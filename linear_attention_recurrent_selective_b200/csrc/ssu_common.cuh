@@ -272,7 +272,7 @@ int launch_ddtree(const TreeArgs &a, int state_dtype, cudaStream_t s);
 int launch_conv_decode(const ConvArgs &a, int state_dtype, cudaStream_t s);
 int launch_conv_prefill(const ConvPrefillArgs &a, int x_dtype, cudaStream_t s);
 int launch_conv_replay(const ConvPrefillArgs &a, int x_dtype, cudaStream_t s);
-int launch_scan_decode(const ScanArgs &a, cudaStream_t s);
+int launch_scan_decode(ScanArgs a, cudaStream_t s);
 int launch_scan_prefill(ScanArgs a, cudaStream_t s);
 int launch_scan_prefill_bf16(const ScanArgs &a, cudaStream_t s);
 int launch_scan_prefill_f16(const ScanArgs &a, cudaStream_t s);

@@ -13,18 +13,27 @@
 // W + 3 multiply-adds and two special-function operations (the sigmoid); windows are
 // touched once per row.
 //
-// Layout: a thread owns one 16-byte vector of channels (VEC = 8 or 4; 1 where rows or
-// segments are not 16-byte aligned) over a strip of up to kStrip tokens, and slides the
+// Layout: a thread owns VEC neighbouring channels (one access of a row; one channel where
+// rows or segments are not aligned) over a strip of up to kStrip tokens, and slides the
 // last W-1 inputs through registers, so each input is read once per strip plus W-1 at the
-// strip's start. The thread of a row's first strip also owns the window of its channels:
+// strip's start. The next tokens' inputs are loaded before the current ones are used. The thread of a row's first strip also owns the window of its channels:
 // it alone reads the old taps (a later strip starts at t >= kStrip >= W-1) and it alone
 // writes the new ones, after its reads, so the update needs no second launch.
+//
+// Over a tree the inputs of a node lie anywhere among the row's nodes: a CTA brings all
+// nodes' rows of 128 bytes of channels to shared memory, with the window's taps as rows
+// before them, so that each input is read from memory once; a thread per node walks its
+// ancestors into a list of rows, and the outputs gather by it.
 #include "ssu_common.cuh"
 
 namespace ssu {
 namespace {
 
+#ifndef HALF
+#define HALF 1
+#endif
 constexpr int kThreads = 128;
+constexpr int kMaxNodes = 128;        // nodes of a draft tree
 constexpr int kStrip = 32;            // tokens of a strip, >= the widest window (16) - 1
 
 template <typename E, int VEC> struct alignas(sizeof(E) * VEC) Chunk {
@@ -42,13 +51,47 @@ template <> __device__ __forceinline__ float widen(float v) { return v; }
 template <> __device__ __forceinline__ float widen(__half v) { return __half2float(v); }
 template <> __device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
 
+// Two neighbouring 16-bit values.
+template <typename E> __device__ __forceinline__ float2 widen_pair(uint32_t w);
+template <> __device__ __forceinline__ float2 widen_pair<__half>(uint32_t w)
+{
+    __half2 h;
+    memcpy(&h, &w, 4);
+    return __half22float2(h);
+}
+template <> __device__ __forceinline__ float2 widen_pair<__nv_bfloat16>(uint32_t w)
+{
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+template <typename E> __device__ __forceinline__ uint32_t narrow_pair(float a, float b);
+template <> __device__ __forceinline__ uint32_t narrow_pair<__half>(float a, float b)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    uint32_t w;
+    memcpy(&w, &h, 4);
+    return w;
+}
+template <> __device__ __forceinline__ uint32_t narrow_pair<__nv_bfloat16>(float a, float b)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    uint32_t w;
+    memcpy(&w, &h, 4);
+    return w;
+}
+
 template <typename E, int VEC>
 __device__ __forceinline__ void widen_chunk(const Chunk<E, VEC> &c, float *f)
 {
-    if constexpr (VEC == Vec16<E>::kElems) {
-        uint4 r;
-        memcpy(&r, &c, 16);
-        Vec16<E>::unpack(r, f);
+    if constexpr (VEC % 2 == 0 && sizeof(E) == 2) {
+        uint32_t w[VEC / 2];
+        memcpy(w, &c, sizeof c);
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+            const float2 v = widen_pair<E>(w[e / 2]);
+            f[e] = v.x;
+            f[e + 1] = v.y;
+        }
     } else {
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
@@ -67,13 +110,19 @@ template <> __device__ __forceinline__ __nv_bfloat16 narrow(float v)
 template <typename E, int VEC>
 __device__ __forceinline__ void store_floats(E *p, const float *f)
 {
-    if constexpr (VEC == Vec16<E>::kElems) {
-        *reinterpret_cast<uint4 *>(p) = Vec16<E>::pack(f);
+    Chunk<E, VEC> c;
+    if constexpr (VEC % 2 == 0 && sizeof(E) == 2) {
+        uint32_t w[VEC / 2];
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2)
+            w[e / 2] = narrow_pair<E>(f[e], f[e + 1]);
+        memcpy(&c, w, sizeof c);
     } else {
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
-            p[e] = narrow<E>(f[e]);
+            c.v[e] = narrow<E>(f[e]);
     }
+    *reinterpret_cast<Chunk<E, VEC> *>(p) = c;
 }
 
 // v * sigmoid(v). 16-bit outputs take the approximate exponential and division, whose
@@ -85,6 +134,25 @@ template <typename E> __device__ __forceinline__ float conv_silu(float v)
         return silu_f(v);
     else
         return __fdividef(v, 1.f + __expf(-v));
+}
+
+// acc += w * f over VEC channels (packed in pairs), and the activation of all of them.
+template <int VEC>
+__device__ __forceinline__ void fma_vec(float (&acc)[VEC], const float (&w)[VEC], const float *f)
+{
+    if constexpr (VEC % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+            const float2 r = __ffma2_rn(make_float2(w[e], w[e + 1]), make_float2(f[e], f[e + 1]),
+                                        make_float2(acc[e], acc[e + 1]));
+            acc[e] = r.x;
+            acc[e + 1] = r.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            acc[e] = fmaf(w[e], f[e], acc[e]);
+    }
 }
 
 // The window taps of VEC channels from channel c0: every tap in registers, oldest first.
@@ -155,6 +223,21 @@ __device__ __forceinline__ void store_taps(const ConvPrefillArgs &a, int64_t at,
     }
 }
 
+// The weights of VEC channels from channel c0 (contiguous), tap by tap.
+template <typename E, int VEC, int W>
+__device__ __forceinline__ void load_weights(const ConvPrefillArgs &a, int c0, float (&w)[W][VEC])
+{
+    Chunk<E, VEC> raw[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+        raw[j] = load_chunk<E, VEC>(a.w, (int64_t)c0 * W + j * VEC);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+            w[k][e] = widen<E>(raw[(e * W + k) / VEC].v[(e * W + k) % VEC]);
+}
+
 // Where a channel's outputs go: x, B and C are separate dense [batch, T, dim] tensors.
 template <typename E> struct OutSeg {
     E *p;               // element (b, t = 0, this channel)
@@ -190,19 +273,8 @@ __device__ __forceinline__ int row_length(const int32_t *len, int b, int T, int 
     return L < 0 ? 0 : (L > T ? T : L);
 }
 
-// The parent of a tree node, -1 at a root. One outside [-1, L) marks the node as malformed;
-// the W-1 steps of a node's walk end whatever the parents hold.
-__device__ __forceinline__ int parent_of(const int32_t *par, int at, int L, bool &bad)
-{
-    const int up = par[at];
-    if (up >= -1 && up < L)
-        return up;
-    bad = true;
-    return -1;
-}
-
 // One thread per (row, strip, vector of channels), widths 2..4.
-template <typename E, int VEC, int W, bool TREE>
+template <typename E, int VEC, int W>
 __global__ void __launch_bounds__(kThreads)
 conv_prefill_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups, const int strips)
 {
@@ -235,15 +307,7 @@ conv_prefill_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups,
 
     float w[W][VEC], bias[VEC];
     {
-        Chunk<E, VEC> raw[W];                   // VEC channels' weights are contiguous
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-            raw[j] = load_chunk<E, VEC>(a.w, (int64_t)c0 * W + j * VEC);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-#pragma unroll
-            for (int k = 0; k < W; ++k)
-                w[k][e] = widen<E>(raw[(e * W + k) / VEC].v[(e * W + k) % VEC]);
+        load_weights<E, VEC, W>(a, c0, w);
         Chunk<E, VEC> rb;
         if (a.bias)
             rb = load_chunk<E, VEC>(a.bias, c0);
@@ -253,48 +317,6 @@ conv_prefill_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups,
     }
     const E *in = static_cast<const E *>(a.xbc) + b * a.T * a.ldx + c0;
     const int64_t tap_at = (int64_t)slot * a.cslot + (int64_t)c0 * a.cc;
-
-    if constexpr (TREE) {
-        const int32_t *par = a.parents + b * a.T;
-        E old[W - 1][VEC];
-        load_taps<E, VEC, W>(a, tap_at, old);
-        for (int t = t0; t < t1; ++t) {
-            float acc[VEC];
-            int at = t;                         // >= 0: a node; -1 - j: j taps back
-            bool bad = false;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                acc[e] = bias[e];
-#pragma unroll
-            for (int k = W - 1; k >= 0; --k) {
-                float f[VEC];
-                if (at >= 0) {
-                    widen_chunk<E, VEC>(load_chunk<E, VEC>(in, at * a.ldx), f);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        f[e] = 0.f;
-#pragma unroll
-                        for (int j = 0; j < W - 1; ++j)
-                            if (at == j - (W - 1))
-                                f[e] = widen<E>(old[j][e]);
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    acc[e] = fmaf(w[k][e], f[e], acc[e]);
-                if (k > 0)
-                    at = at >= 0 ? parent_of(par, at, L, bad) : at - 1;
-            }
-            if (bad && g == 0 && a.err)
-                atomicOr(a.err, SSU_FLAG_TREE);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                acc[e] = bad ? 0.f : (a.silu ? conv_silu<E>(acc[e]) : acc[e]);
-            store_floats<E, VEC>(out.p + t * out.ld, acc);
-        }
-        return;
-    }
 
     float win[W - 1][VEC];                      // in[t - (W-1)] .. in[t - 1]
     E old[W - 1][VEC];
@@ -311,13 +333,17 @@ conv_prefill_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups,
             widen_chunk<E, VEC>(load_chunk<E, VEC>(in, (t0 - (W - 1) + j) * a.ldx), win[j]);
     }
 
-    constexpr int U = 4;                        // tokens loaded together
+    constexpr int U = 4;                        // tokens loaded together, a round ahead
+    Chunk<E, VEC> raw[U], next[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (t0 + u < t1)
+            raw[u] = load_chunk<E, VEC>(in, (t0 + u) * a.ldx);
     for (int t = t0; t < t1; t += U) {
-        Chunk<E, VEC> raw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (t + u < t1)
-                raw[u] = load_chunk<E, VEC>(in, (t + u) * a.ldx);
+            if (t + U + u < t1)
+                next[u] = load_chunk<E, VEC>(in, (t + U + u) * a.ldx);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (t + u >= t1)
@@ -325,14 +351,19 @@ conv_prefill_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups,
             float f[VEC], acc[VEC];
             widen_chunk<E, VEC>(raw[u], f);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
+            for (int e = 0; e < VEC; ++e)
                 acc[e] = bias[e];
 #pragma unroll
-                for (int k = 0; k < W - 1; ++k)
-                    acc[e] = fmaf(w[k][e], win[k][e], acc[e]);
-                acc[e] = fmaf(w[W - 1][e], f[e], acc[e]);
-                if (a.silu)
+            for (int k = 0; k < W - 1; ++k)
+                fma_vec<VEC>(acc, w[k], win[k]);
+            fma_vec<VEC>(acc, w[W - 1], f);
+            if (a.silu) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
                     acc[e] = conv_silu<E>(acc[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
 #pragma unroll
                 for (int k = 0; k + 1 < W - 1; ++k)
                     win[k][e] = win[k + 1][e];
@@ -340,6 +371,9 @@ conv_prefill_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups,
             }
             store_floats<E, VEC>(out.p + (t + u) * out.ld, acc);
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            raw[u] = next[u];
     }
 
     if (strip == 0 && a.update) {               // the last W-1 of (old taps, tokens)
@@ -367,7 +401,7 @@ conv_prefill_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups,
 
 // Every other width (1, 5..16): a thread per (row, strip, channel) that reads each tap
 // where it lies. Same ownership of the windows.
-template <typename E, bool TREE>
+template <typename E>
 __global__ void __launch_bounds__(kThreads)
 conv_prefill_any_kernel(const __grid_constant__ ConvPrefillArgs a, const int channels,
                         const int strips)
@@ -401,26 +435,173 @@ conv_prefill_any_kernel(const __grid_constant__ ConvPrefillArgs a, const int cha
     const E *w = static_cast<const E *>(a.w) + (int64_t)c * W;
     const float bias = a.bias ? widen<E>(static_cast<const E *>(a.bias)[c]) : 0.f;
     E *tap = static_cast<E *>(a.cstate) + (int64_t)slot * a.cslot + (int64_t)c * a.cc;
-    const int32_t *par = TREE ? a.parents + b * a.T : nullptr;
     for (int t = t0; t < t1; ++t) {
         float acc = bias;
-        int at = t;
-        bool bad = false;
-        for (int k = W - 1; k >= 0; --k) {
-            const float f = at >= 0 ? widen<E>(in[at * a.ldx]) : widen<E>(tap[(at + W - 1) * a.ck]);
-            acc = fmaf(widen<E>(w[k]), f, acc);
-            if (k > 0)
-                at = TREE && at >= 0 ? parent_of(par, at, L, bad) : at - 1;
-        }
-        if (bad && c == 0 && a.err)
-            atomicOr(a.err, SSU_FLAG_TREE);
-        out.p[t * out.ld] = narrow<E>(bad ? 0.f : (a.silu ? conv_silu<E>(acc) : acc));
+        for (int k = W - 1, at = t; k >= 0; --k, --at)
+            acc = fmaf(widen<E>(w[k]),
+                       at >= 0 ? widen<E>(in[at * a.ldx]) : widen<E>(tap[(at + W - 1) * a.ck]), acc);
+        out.p[t * out.ld] = narrow<E>(a.silu ? conv_silu<E>(acc) : acc);
     }
-    if (!TREE && strip == 0 && a.update)
+    if (strip == 0 && a.update)
         for (int j = 0; j < W - 1; ++j) {       // ascending: a tap is read before it is replaced
             const int t = L + j - (W - 1);
             tap[j * a.ck] = t >= 0 ? in[t * a.ldx] : tap[(L + j) * a.ck];
         }
+}
+
+// A CTA per (row, 128 bytes of channels) of a draft tree of up to kMaxNodes nodes. W: the
+// width, or 0 for any.
+template <typename E, int W>
+__global__ void __launch_bounds__(kThreads)
+conv_tree_kernel(const __grid_constant__ ConvPrefillArgs a, const int blocks, const bool vec)
+{
+    constexpr int V = Vec16<E>::kElems, kCh = 8 * V, kUnits = 8;
+    constexpr int kMaxW = W ? W : 16;
+    __shared__ __align__(16) E s_in[(kMaxNodes + kMaxW - 1) * kCh];
+    __shared__ uint8_t s_row[kMaxNodes][kMaxW];         // rows of the inputs, newest first
+    __shared__ uint8_t s_bad[kMaxNodes];
+    __shared__ int s_par[kMaxNodes];
+    const int width = W ? W : a.width, taps = width - 1;
+    const int b = blockIdx.x / blocks, tid = threadIdx.x;
+    const int c0 = (blockIdx.x % blocks) * kCh, channels = a.x_dim + 2 * a.bc_dim;
+    const bool first = blockIdx.x % blocks == 0 && tid == 0;
+    const int slot = a.idx ? a.idx[b] : b;
+    if (slot >= a.P) {                          // caller bug: skip the row and report it
+        if (first && a.err)
+            atomicOr(a.err, SSU_FLAG_INDEX_RANGE);
+        return;
+    }
+    // this thread's unit of V channels, and where its outputs go
+    const int u = tid % kUnits, cu = c0 + u * V;
+    const auto store = [&](int t, const float (&f)[V]) {
+        if (vec && cu < channels) {             // whole and inside one segment
+            const OutSeg<E> o = out_seg<E>(a, b, cu);
+            store_floats<E, V>(o.p + t * o.ld, f);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (cu + e < channels) {
+                    const OutSeg<E> o = out_seg<E>(a, b, cu + e);
+                    o.p[t * o.ld] = narrow<E>(f[e]);
+                }
+        }
+    };
+    if (slot < 0) {                             // padding row: zeros
+        const float zero[V] = {};
+        for (int t = tid / kUnits; t < a.T; t += kThreads / kUnits)
+            store(t, zero);
+        return;
+    }
+    const int L = row_length(a.ctx, b, a.T, SSU_FLAG_CONTEXT_RANGE, first, a.err);
+    if (L == 0)
+        return;
+
+    const E *const in = static_cast<const E *>(a.xbc) + (int64_t)b * a.T * a.ldx + c0;
+    const int left = min(kCh, channels - c0);
+    if (vec) {
+        for (int i = tid; i < L * kUnits; i += kThreads) {
+            const int t = i / kUnits, e = i % kUnits * V;
+            if (e < left) {
+                const uint32_t d = (uint32_t)__cvta_generic_to_shared(s_in + (taps + t) * kCh + e);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d),
+                             "l"(in + t * a.ldx + e)
+                             : "memory");
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    } else {
+        for (int i = tid; i < L * kCh; i += kThreads)
+            if (i % kCh < left)
+                s_in[(taps + i / kCh) * kCh + i % kCh] = in[i / kCh * a.ldx + i % kCh];
+    }
+    const E *const tap = static_cast<const E *>(a.cstate) + (int64_t)slot * a.cslot +
+                         (int64_t)c0 * a.cc;
+    for (int i = tid; i < taps * kCh; i += kThreads)
+        if (i % kCh < left)
+            s_in[i] = tap[i % kCh * a.cc + i / kCh * a.ck];
+    if (tid < L)
+        s_par[tid] = a.parents[(int64_t)b * a.T + tid];
+
+    float w[W ? W : 1][V], bias[V];
+    if (vec) {                                  // (a unit beyond the last repeats it)
+        const int c = min(cu, channels - V);
+        Chunk<E, V> rb;
+        if (a.bias)
+            rb = load_chunk<E, V>(a.bias, c);
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            bias[e] = a.bias ? widen<E>(rb.v[e]) : 0.f;
+        if constexpr (W > 0)
+            load_weights<E, V, W>(a, c, w);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const int c = min(cu + e, channels - 1);
+            bias[e] = a.bias ? widen<E>(static_cast<const E *>(a.bias)[c]) : 0.f;
+            if constexpr (W > 0) {
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+                    w[k][e] = widen<E>(static_cast<const E *>(a.w)[(int64_t)c * W + k]);
+            }
+        }
+    }
+    __syncthreads();
+    // the rows of a node's inputs: nodes from row `taps` on, taps before them (so a parent of
+    // -1 is the newest tap). A parent outside [-1, L) marks the node as malformed; the walk
+    // takes width - 1 steps whatever the parents hold.
+    if (tid < L) {
+        int at = tid;
+        bool bad = false;
+        for (int k = 0; k < width; ++k) {
+            s_row[tid][k] = (uint8_t)(at + taps);
+            if (k + 1 < width) {
+                if (at >= 0) {
+                    at = s_par[at];
+                    if (at < -1 || at >= L) {
+                        bad = true;
+                        at = -1;
+                    }
+                } else {
+                    --at;
+                }
+            }
+        }
+        s_bad[tid] = bad;
+        if (bad && c0 == 0 && a.err)
+            atomicOr(a.err, SSU_FLAG_TREE);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+
+    for (int t = tid / kUnits; t < L; t += kThreads / kUnits) {
+        float acc[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            acc[e] = bias[e];
+        const auto add = [&](int k, const float (&wk)[V]) {
+            float f[V];
+            widen_chunk<E, V>(load_chunk<E, V>(s_in, s_row[t][width - 1 - k] * kCh + u * V), f);
+            fma_vec<V>(acc, wk, f);
+        };
+        if constexpr (W > 0) {
+#pragma unroll
+            for (int k = 0; k < W; ++k)
+                add(k, w[k]);
+        } else {
+            for (int k = 0; k < width; ++k) {
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    w[0][e] = widen<E>(
+                        static_cast<const E *>(a.w)[(int64_t)min(cu + e, channels - 1) * width + k]);
+                add(k, w[0]);
+            }
+        }
+        const bool bad = s_bad[t];
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            acc[e] = bad ? 0.f : (a.silu ? conv_silu<E>(acc[e]) : acc[e]);
+        store(t, acc);
+    }
 }
 
 // Commit: the window becomes the last W-1 of (window, first k_b accepted tokens). A block
@@ -524,17 +705,22 @@ int launch_w(const ConvPrefillArgs &a, cudaStream_t s)
     const int64_t blocks = ((int64_t)groups * strips * a.active + kThreads - 1) / kThreads;
     if (blocks > 0x7fffffffLL)
         return SSU_ERR_SHAPE;
-    if constexpr (W == 0) {
-        return a.parents ? launch_kernel(conv_prefill_any_kernel<E, true>, (unsigned)blocks,
-                                         kThreads, 0, s, a, groups, strips)
-                         : launch_kernel(conv_prefill_any_kernel<E, false>, (unsigned)blocks,
-                                         kThreads, 0, s, a, groups, strips);
-    } else {
-        return a.parents ? launch_kernel(conv_prefill_kernel<E, VEC, W, true>, (unsigned)blocks,
-                                         kThreads, 0, s, a, groups, strips)
-                         : launch_kernel(conv_prefill_kernel<E, VEC, W, false>, (unsigned)blocks,
-                                         kThreads, 0, s, a, groups, strips);
-    }
+    if constexpr (W == 0)
+        return launch_kernel(conv_prefill_any_kernel<E>, (unsigned)blocks, kThreads, 0, s, a, groups,
+                             strips);
+    else
+        return launch_kernel(conv_prefill_kernel<E, VEC, W>, (unsigned)blocks, kThreads, 0, s, a,
+                             groups, strips);
+}
+
+template <typename E, int W> int launch_tree(const ConvPrefillArgs &a, bool vec, cudaStream_t s)
+{
+    const int per = 8 * Vec16<E>::kElems;
+    const int blocks = (a.x_dim + 2 * a.bc_dim + per - 1) / per;
+    if ((int64_t)blocks * a.active > 0x7fffffffLL)
+        return SSU_ERR_SHAPE;
+    return launch_kernel(conv_tree_kernel<E, W>, (unsigned)(blocks * a.active), kThreads, 0, s, a,
+                         blocks, vec);
 }
 
 template <typename E, int VEC>
@@ -550,10 +736,19 @@ int launch_v(const ConvPrefillArgs &a, cudaStream_t s)
 
 template <typename E> int launch_e(ConvPrefillArgs a, cudaStream_t s)
 {
-    if (!vector_rows<E>(a))
+    const bool vec = vector_rows<E>(a);
+    if (a.parents) {
+        switch (a.width) {
+        case 2: return launch_tree<E, 2>(a, vec, s);
+        case 3: return launch_tree<E, 3>(a, vec, s);
+        case 4: return launch_tree<E, 4>(a, vec, s);
+        default: return launch_tree<E, 0>(a, vec, s);
+        }
+    }
+    if (!vec)
         return launch_v<E, 1>(a, s);
     a.win_mode = window_mode<E>(a);
-    return launch_v<E, Vec16<E>::kElems>(a, s);
+    return launch_v<E, Vec16<E>::kElems / HALF>(a, s);
 }
 
 template <typename E, int VEC, int W>

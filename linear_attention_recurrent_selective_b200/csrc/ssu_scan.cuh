@@ -58,42 +58,10 @@ __device__ __forceinline__ float2 softplus2(float2 v)
     return fma2(add2(s, s), p, make_float2(v.x < 0.f ? 0.f : v.x, v.y < 0.f ? 0.f : v.y));
 }
 
-__device__ __forceinline__ float softplus_scan(float v) { return softplus2(both(v)).x; }
-
-// 2^v for two values by a polynomial on the multiply-add pipe, for part of a warp's
-// exponentials when the special-function unit is what the rest waits for: v = n + f with
-// |f| <= 1/2 by adding and subtracting 1.5 * 2^23 (round to nearest, n left in the low
-// bits), 2^f by the minimax polynomial of degree 5 that starts with 1 (relative error
-// 2^-23.4), and a multiplication by 2^n. Below -126 the result is 2^-126 for 0, from 128 on
-// infinity; a NaN stays one.
-__device__ __forceinline__ float2 exp2_poly2(float2 v)
-{
-    const float kMagic = 12582912.f;
-    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(v.x));          // -126
-    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(v.y));
-    asm("min.NaN.f32 %0, %0, 0f43000000;" : "+f"(v.x));          // 128
-    asm("min.NaN.f32 %0, %0, 0f43000000;" : "+f"(v.y));
-    const float2 r = add2(v, both(kMagic));
-    const float2 n = add2(r, both(-kMagic));
-    const float2 f = add2(v, make_float2(-n.x, -n.y));
-    float2 p = fma2(f, both(0.001326472731f), both(0.009671512991f));
-    p = fma2(p, f, both(0.05550733581f));
-    p = fma2(p, f, both(0.2402224243f));
-    p = fma2(p, f, both(0.6931470037f));
-    p = fma2(p, f, both(1.f));
-    const float2 s = make_float2(__int_as_float((__float_as_int(r.x) << 23) + 0x3f800000),
-                                 __int_as_float((__float_as_int(r.y) << 23) + 0x3f800000));
-    return mul2(p, s);
-}
-
-// silu with the approximate exponential and division: relative error below 2^-20 for
-// |z| < 20, which a 16-bit output's rounding (2^-9 or 2^-11) hides; fp32 outputs take the
-// accurate one. (Far below zero the reciprocal of 2^127 and more is 0, and so is the gate.)
-__device__ __forceinline__ float gate(float z, int out_dtype)
-{
-    return out_dtype == SSU_F32 ? silu_f(z) : z * rcp_fast(1.f + exp2_fast(-1.44269504f * z));
-}
-
+// silu of two values, with the approximate exponential and reciprocal: relative error below
+// 2^-20 for |z| < 20, which a 16-bit output's rounding (2^-9 or 2^-11) hides; fp32 outputs
+// take the accurate one. (Far below zero the reciprocal of 2^127 and more is 0, and so is
+// the gate.)
 __device__ __forceinline__ float2 gate2(float2 z, int out_dtype)
 {
     if (out_dtype == SSU_F32)
@@ -101,6 +69,59 @@ __device__ __forceinline__ float2 gate2(float2 z, int out_dtype)
     const float2 m = mul2(z, both(-1.44269504f));
     const float2 e = add2(make_float2(exp2_fast(m.x), exp2_fast(m.y)), both(1.f));
     return mul2(z, make_float2(rcp_fast(e.x), rcp_fast(e.y)));
+}
+
+// The lanes of a channel share out four items (tokens of a prompt, rows of a batch): a lane
+// forms the scalars of its own, hands them to the others and gets back their sums.
+
+// Of four items, the i-th that lane ln of a channel owns (lanes beyond the fourth repeat).
+template <int kL> __device__ __forceinline__ int own(int ln, int i)
+{
+    return kL == 1 ? i : kL == 2 ? ln + 2 * i : ln & 3;
+}
+
+// Value of item u (of four) and channel c from the lane that owns it; v: this lane's own.
+template <int kL, int CH, int kPr>
+__device__ __forceinline__ float of_item(const float2 (&v)[kPr], int u, int c)
+{
+    const int i = kL == 1 ? u : kL == 2 ? u >> 1 : 0;       // its index at the owner
+    const float w = CH == 2 ? (c ? v[i].y : v[i].x) : (i & 1 ? v[i >> 1].y : v[i >> 1].x);
+    return kL == 1 ? w : __shfl_sync(~0u, w, kL == 2 ? u & 1 : u, kL);
+}
+
+// Sums over the lanes of a channel of four values (four items) of CH channels: each lane
+// gets those of its own items. At each of the first two steps a lane hands half of its
+// values to its partner.
+template <int kL, int CH, int kPr>
+__device__ __forceinline__ void sum_own(const float (&v)[CH][4], float2 (&s)[kPr], int ln)
+{
+    float own[CH][4];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        if constexpr (kL == 1) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                own[c][u] = v[c][u];
+        } else {
+            const bool hi = ln & 1;                         // odd items
+            const float g0 = __shfl_xor_sync(~0u, hi ? v[c][0] : v[c][1], 1);
+            const float g1 = __shfl_xor_sync(~0u, hi ? v[c][2] : v[c][3], 1);
+            own[c][0] = (hi ? v[c][1] : v[c][0]) + g0;
+            own[c][1] = (hi ? v[c][3] : v[c][2]) + g1;
+            if constexpr (kL >= 4) {
+                const bool h2 = ln & 2;                     // items 2, 3
+                const float g = __shfl_xor_sync(~0u, h2 ? own[c][0] : own[c][1], 2);
+                own[c][0] = (h2 ? own[c][1] : own[c][0]) + g;
+#pragma unroll
+                for (int o = 4; o < kL; o <<= 1)
+                    own[c][0] += __shfl_xor_sync(~0u, own[c][0], o);
+            }
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < kPr; ++p)
+        s[p] = CH == 2 ? make_float2(own[0][p], own[CH - 1][p])
+                       : make_float2(own[0][2 * p], own[0][kL >= 4 ? 0 : 2 * p + 1]);
 }
 
 // kS consecutive states (4, or 8) of a channel, in the pool's type. The element offset is

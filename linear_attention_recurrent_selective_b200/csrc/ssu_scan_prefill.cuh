@@ -193,56 +193,6 @@ __device__ __forceinline__ void widen_rows(float *dst, const uint8_t *raw, int d
     }
 }
 
-// Of four tokens, the i-th that lane ln of a channel owns (lanes beyond the fourth repeat).
-template <int kL> __device__ __forceinline__ int own(int ln, int i)
-{
-    return kL == 1 ? i : kL == 2 ? ln + 2 * i : ln & 3;
-}
-
-// Value of token u (of four) and channel c from the lane that owns it; v: this lane's own.
-template <int kL, int CH, int kPr>
-__device__ __forceinline__ float of_token(const float2 (&v)[kPr], int u, int c)
-{
-    const int i = kL == 1 ? u : kL == 2 ? u >> 1 : 0;       // its index at the owner
-    const float w = CH == 2 ? (c ? v[i].y : v[i].x) : (i & 1 ? v[i >> 1].y : v[i >> 1].x);
-    return kL == 1 ? w : __shfl_sync(~0u, w, kL == 2 ? u & 1 : u, kL);
-}
-
-// Sums over the lanes of a channel of four values (four tokens) of CH channels: each lane
-// gets those of its own tokens. At each of the first two steps a lane hands half of its
-// values to its partner.
-template <int kL, int CH, int kPr>
-__device__ __forceinline__ void sum_own(const float (&v)[CH][4], float2 (&s)[kPr], int ln)
-{
-    float own[CH][4];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        if constexpr (kL == 1) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                own[c][u] = v[c][u];
-        } else {
-            const bool hi = ln & 1;                         // odd tokens
-            const float g0 = __shfl_xor_sync(~0u, hi ? v[c][0] : v[c][1], 1);
-            const float g1 = __shfl_xor_sync(~0u, hi ? v[c][2] : v[c][3], 1);
-            own[c][0] = (hi ? v[c][1] : v[c][0]) + g0;
-            own[c][1] = (hi ? v[c][3] : v[c][2]) + g1;
-            if constexpr (kL >= 4) {
-                const bool h2 = ln & 2;                     // tokens 2, 3
-                const float g = __shfl_xor_sync(~0u, h2 ? own[c][0] : own[c][1], 2);
-                own[c][0] = (h2 ? own[c][1] : own[c][0]) + g;
-#pragma unroll
-                for (int o = 4; o < kL; o <<= 1)
-                    own[c][0] += __shfl_xor_sync(~0u, own[c][0], o);
-            }
-        }
-    }
-#pragma unroll
-    for (int p = 0; p < kPr; ++p)
-        s[p] = CH == 2 ? make_float2(own[0][p], own[CH - 1][p])
-                       : make_float2(own[0][2 * p], own[0][kL >= 4 ? 0 : 2 * p + 1]);
-}
-
 // Length used to order the rows: padding and out-of-range rows do (almost) no work.
 __device__ __forceinline__ int sched_len(const ScanArgs &a, int b)
 {
@@ -402,8 +352,8 @@ __device__ __forceinline__ void run_tokens(const ScanArgs &a, Lane<CH> &st, uint
                 }
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
-                    const float2 d2 = both(of_token<kL, CH, kPr>(dt, u, c));
-                    const float2 x2 = both(of_token<kL, CH, kPr>(dx, u, c));
+                    const float2 d2 = both(of_item<kL, CH, kPr>(dt, u, c));
+                    const float2 x2 = both(of_item<kL, CH, kPr>(dx, u, c));
                     float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int i = 0; i < kP; ++i) {

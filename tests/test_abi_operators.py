@@ -36,6 +36,7 @@ CONV = dict(xbc=P16, dt=2, ld=5376, w=P16, bias=None, pool=P16, cs=5376 * 3, cc=
     (dict(active=-1), 2), (dict(T=-1), 2), (dict(xd=0), 2), (dict(bc=-1), 2), (dict(P=-1), 2),
     (dict(idx=None, P=15), 2), (dict(cs=5376 * 3 - 1), 2), (dict(cc=2), 2), (dict(ck=0), 2),
     (dict(cc=1, ck=5375), 2), (dict(cc=-3), 2), (dict(par=P16), 2),
+    (dict(par=P16, upd=0, T=129), 2),
     (dict(cc=1 << 62, cs=(1 << 62) + 5), 2), (dict(xd=2 ** 31 - 1, bc=2 ** 30, ld=2 ** 40), 2),
 ])
 def test_conv_prefill(L, kw, status):
