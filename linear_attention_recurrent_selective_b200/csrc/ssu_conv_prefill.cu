@@ -24,16 +24,14 @@
 // nodes' rows of 128 bytes of channels to shared memory, with the window's taps as rows
 // before them, so that each input is read from memory once; a thread per node walks its
 // ancestors into a list of rows, and the outputs gather by it.
-#include "ssu_common.cuh"
+#include "ssu_math.cuh"
 
 namespace ssu {
 namespace {
 
-#ifndef HALF
-#define HALF 1
-#endif
 constexpr int kThreads = 128;
 constexpr int kMaxNodes = 128;        // nodes of a draft tree
+constexpr int kStages = 3, kGroup = 4;  // of a thread's ring
 constexpr int kStrip = 32;            // tokens of a strip, >= the widest window (16) - 1
 
 template <typename E, int VEC> struct alignas(sizeof(E) * VEC) Chunk {
@@ -125,26 +123,37 @@ __device__ __forceinline__ void store_floats(E *p, const float *f)
     *reinterpret_cast<Chunk<E, VEC> *>(p) = c;
 }
 
-// v * sigmoid(v). 16-bit outputs take the approximate exponential and division, whose
-// error (a few 2^-22) is far below the 2^-9 of the rounding that follows; fp32 outputs
-// take the accurate ones.
+// v * sigmoid(v) for an output of type E.
 template <typename E> __device__ __forceinline__ float conv_silu(float v)
 {
-    if constexpr (sizeof(E) == 4)
-        return silu_f(v);
-    else
-        return __fdividef(v, 1.f + __expf(-v));
+    return silu2<sizeof(E) == 4>(both(v)).x;
 }
 
-// acc += w * f over VEC channels (packed in pairs), and the activation of all of them.
+template <typename E, int VEC> __device__ __forceinline__ void silu_vec(float (&v)[VEC])
+{
+    if constexpr (VEC % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+            const float2 r = silu2<sizeof(E) == 4>(make_float2(v[e], v[e + 1]));
+            v[e] = r.x;
+            v[e + 1] = r.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            v[e] = conv_silu<E>(v[e]);
+    }
+}
+
+// acc += w * f over VEC channels (packed in pairs).
 template <int VEC>
 __device__ __forceinline__ void fma_vec(float (&acc)[VEC], const float (&w)[VEC], const float *f)
 {
     if constexpr (VEC % 2 == 0) {
 #pragma unroll
         for (int e = 0; e < VEC; e += 2) {
-            const float2 r = __ffma2_rn(make_float2(w[e], w[e + 1]), make_float2(f[e], f[e + 1]),
-                                        make_float2(acc[e], acc[e + 1]));
+            const float2 r = fma2(make_float2(w[e], w[e + 1]), make_float2(f[e], f[e + 1]),
+                                  make_float2(acc[e], acc[e + 1]));
             acc[e] = r.x;
             acc[e + 1] = r.y;
         }
@@ -155,6 +164,10 @@ __device__ __forceinline__ void fma_vec(float (&acc)[VEC], const float (&w)[VEC]
     }
 }
 
+// The widest access (at most 16 bytes) that whole runs of `bytes` contiguous bytes from one
+// multiple of `bytes` to the next can be cut into.
+constexpr int access(int bytes) { return bytes % 16 == 0 ? 16 : bytes % 8 == 0 ? 8 : bytes % 4 == 0 ? 4 : 2; }
+
 // The window taps of VEC channels from channel c0: every tap in registers, oldest first.
 // mode 1: channel-major windows (stride_c = W-1, stride_k = 1), the VEC * (W-1) elements
 // contiguous and 16-byte aligned; mode 2: tap-major (stride_c = 1), a vector per tap;
@@ -164,15 +177,16 @@ __device__ __forceinline__ void load_taps(const ConvPrefillArgs &a, int64_t at, 
 {
     const E *p = static_cast<const E *>(a.cstate) + at;
     if (a.win_mode == 1) {
-        Chunk<E, VEC> raw[W - 1];
+        constexpr int kAll = VEC * (W - 1), kC = access(kAll * sizeof(E)) / sizeof(E);
+        Chunk<E, kC> raw[kAll / kC];
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j)
-            raw[j] = load_chunk<E, VEC>(p, j * VEC);
+        for (int j = 0; j < kAll / kC; ++j)
+            raw[j] = load_chunk<E, kC>(p, j * kC);
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
 #pragma unroll
             for (int k = 0; k < W - 1; ++k)
-                tap[k][e] = raw[(e * (W - 1) + k) / VEC].v[(e * (W - 1) + k) % VEC];
+                tap[k][e] = raw[(e * (W - 1) + k) / kC].v[(e * (W - 1) + k) % kC];
     } else if (a.win_mode == 2) {
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
@@ -196,15 +210,16 @@ __device__ __forceinline__ void store_taps(const ConvPrefillArgs &a, int64_t at,
 {
     E *p = static_cast<E *>(a.cstate) + at;
     if (a.win_mode == 1) {
-        Chunk<E, VEC> raw[W - 1];
+        constexpr int kAll = VEC * (W - 1), kC = access(kAll * sizeof(E)) / sizeof(E);
+        Chunk<E, kC> raw[kAll / kC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
 #pragma unroll
             for (int k = 0; k < W - 1; ++k)
-                raw[(e * (W - 1) + k) / VEC].v[(e * (W - 1) + k) % VEC] = tap[k][e];
+                raw[(e * (W - 1) + k) / kC].v[(e * (W - 1) + k) % kC] = tap[k][e];
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j)
-            *reinterpret_cast<Chunk<E, VEC> *>(p + j * VEC) = raw[j];
+        for (int j = 0; j < kAll / kC; ++j)
+            *reinterpret_cast<Chunk<E, kC> *>(p + j * kC) = raw[j];
     } else if (a.win_mode == 2) {
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
@@ -227,15 +242,40 @@ __device__ __forceinline__ void store_taps(const ConvPrefillArgs &a, int64_t at,
 template <typename E, int VEC, int W>
 __device__ __forceinline__ void load_weights(const ConvPrefillArgs &a, int c0, float (&w)[W][VEC])
 {
-    Chunk<E, VEC> raw[W];
+    constexpr int kAll = VEC * W, kC = access(kAll * sizeof(E)) / sizeof(E);
+    Chunk<E, kC> raw[kAll / kC];
 #pragma unroll
-    for (int j = 0; j < W; ++j)
-        raw[j] = load_chunk<E, VEC>(a.w, (int64_t)c0 * W + j * VEC);
+    for (int j = 0; j < kAll / kC; ++j)
+        raw[j] = load_chunk<E, kC>(a.w, (int64_t)c0 * W + j * kC);
 #pragma unroll
     for (int e = 0; e < VEC; ++e)
 #pragma unroll
         for (int k = 0; k < W; ++k)
-            w[k][e] = widen<E>(raw[(e * W + k) / VEC].v[(e * W + k) % VEC]);
+            w[k][e] = widen<E>(raw[(e * W + k) / kC].v[(e * W + k) % kC]);
+}
+
+// The window after n inputs have passed through it: the last W-1 of (old taps, inputs).
+template <typename E, int VEC, int W, typename Input>
+__device__ __forceinline__ void new_taps(const E (&old)[W - 1][VEC], E (&nw)[W - 1][VEC], int n,
+                                         const Input &input)
+{
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+        const int t = n + j - (W - 1);          // < 0: still an old tap
+        if (t >= 0) {
+            const Chunk<E, VEC> c = input(t);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                nw[j][e] = c.v[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+#pragma unroll
+                for (int o = 0; o < W - 1; ++o)
+                    if (o == n + j)
+                        nw[j][e] = old[o][e];
+        }
+    }
 }
 
 // Where a channel's outputs go: x, B and C are separate dense [batch, T, dim] tensors.
@@ -273,8 +313,8 @@ __device__ __forceinline__ int row_length(const int32_t *len, int b, int T, int 
     return L < 0 ? 0 : (L > T ? T : L);
 }
 
-// One thread per (row, strip, vector of channels), widths 2..4.
-template <typename E, int VEC, int W>
+// One thread per (row, strip, vector of channels), widths 2..4; U: tokens loaded together.
+template <typename E, int VEC, int W, int U>
 __global__ void __launch_bounds__(kThreads)
 conv_prefill_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups, const int strips)
 {
@@ -333,70 +373,175 @@ conv_prefill_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups,
             widen_chunk<E, VEC>(load_chunk<E, VEC>(in, (t0 - (W - 1) + j) * a.ldx), win[j]);
     }
 
-    constexpr int U = 4;                        // tokens loaded together, a round ahead
-    Chunk<E, VEC> raw[U], next[U];
+    const auto token = [&](const Chunk<E, VEC> &raw, int t) {
+        float f[VEC], acc[VEC];
+        widen_chunk<E, VEC>(raw, f);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (t0 + u < t1)
-            raw[u] = load_chunk<E, VEC>(in, (t0 + u) * a.ldx);
-    for (int t = t0; t < t1; t += U) {
+        for (int e = 0; e < VEC; ++e)
+            acc[e] = bias[e];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (t + U + u < t1)
-                next[u] = load_chunk<E, VEC>(in, (t + U + u) * a.ldx);
+        for (int k = 0; k < W - 1; ++k)
+            fma_vec<VEC>(acc, w[k], win[k]);
+        fma_vec<VEC>(acc, w[W - 1], f);
+        if (a.silu)
+            silu_vec<E, VEC>(acc);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (t + u >= t1)
-                break;
-            float f[VEC], acc[VEC];
-            widen_chunk<E, VEC>(raw[u], f);
+        for (int e = 0; e < VEC; ++e) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                acc[e] = bias[e];
-#pragma unroll
-            for (int k = 0; k < W - 1; ++k)
-                fma_vec<VEC>(acc, w[k], win[k]);
-            fma_vec<VEC>(acc, w[W - 1], f);
-            if (a.silu) {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    acc[e] = conv_silu<E>(acc[e]);
-            }
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-#pragma unroll
-                for (int k = 0; k + 1 < W - 1; ++k)
-                    win[k][e] = win[k + 1][e];
-                win[W - 2][e] = f[e];
-            }
-            store_floats<E, VEC>(out.p + (t + u) * out.ld, acc);
+            for (int k = 0; k + 1 < W - 1; ++k)
+                win[k][e] = win[k + 1][e];
+            win[W - 2][e] = f[e];
         }
+        store_floats<E, VEC>(out.p + t * out.ld, acc);
+    };
+    int t = t0;
+    if constexpr (U > 1) {                      // groups of U tokens, loaded a round ahead
+        Chunk<E, VEC> raw[U], next[U];
+        if (t + U <= t1) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            raw[u] = next[u];
+            for (int u = 0; u < U; ++u)
+                raw[u] = load_chunk<E, VEC>(in, (t + u) * a.ldx);
+        }
+        for (; t + U <= t1; t += U) {
+            if (t + 2 * U <= t1) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    next[u] = load_chunk<E, VEC>(in, (t + U + u) * a.ldx);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                token(raw[u], t + u);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                raw[u] = next[u];
+        }
     }
+    for (; t < t1; ++t)
+        token(load_chunk<E, VEC>(in, t * a.ldx), t);
 
-    if (strip == 0 && a.update) {               // the last W-1 of (old taps, tokens)
+    if (strip == 0 && a.update) {
         E nw[W - 1][VEC];
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j) {
-            const int t = L + j - (W - 1);      // < 0: still an old tap
-            if (t >= 0) {
-                const Chunk<E, VEC> c = load_chunk<E, VEC>(in, t * a.ldx);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    nw[j][e] = c.v[e];
-            } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-#pragma unroll
-                    for (int o = 0; o < W - 1; ++o)
-                        if (o == L + j)
-                            nw[j][e] = old[o][e];
-            }
-        }
+        new_taps<E, VEC, W>(old, nw, L, [&](int p) { return load_chunk<E, VEC>(in, p * a.ldx); });
         store_taps<E, VEC, W>(a, tap_at, nw);
     }
+}
+
+// The same for whole 16-byte vectors and long rows: each thread streams its vectors of the
+// strip through a ring of its own in shared memory by cp.async, kStages groups of kGroup
+// tokens ahead, so that what is in flight does not take registers (a register prefetch of
+// one group kept 14 KB an SM in flight: 60 us for 16 rows of 512 tokens of 5376 channels in
+// bfloat16, against 43 us this way). Only its own copies are waited for: no barrier.
+template <typename E, int W>
+__global__ void __launch_bounds__(kThreads)
+conv_stream_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups, const int strips)
+{
+    constexpr int VEC = Vec16<E>::kElems;
+    __shared__ Chunk<E, VEC> ring[kStages * kGroup][kThreads];
+    const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int g = (int)(id % groups);
+    const int64_t rs = id / groups;
+    const int strip = (int)(rs % strips);
+    const int64_t b = rs / strips;
+    if (b >= a.active)
+        return;
+    const int c0 = g * VEC, t0 = strip * kStrip;
+    const bool first = strip == 0 && g == 0;
+    const int slot = a.idx ? a.idx[b] : (int)b;
+    if (slot >= a.P) {                          // caller bug: skip the row and report it
+        if (first && a.err)
+            atomicOr(a.err, SSU_FLAG_INDEX_RANGE);
+        return;
+    }
+    const OutSeg<E> out = out_seg<E>(a, b, c0);
+    if (slot < 0) {                             // padding row: zeros at every token
+        float zero[VEC] = {};
+        for (int t = t0; t < min(t0 + kStrip, a.T); ++t)
+            store_floats<E, VEC>(out.p + t * out.ld, zero);
+        return;
+    }
+    const int L = row_length(a.ctx, (int)b, a.T, SSU_FLAG_CONTEXT_RANGE, first, a.err);
+    const int t1 = min(t0 + kStrip, L);
+    if (t0 >= L)
+        return;
+
+    const E *in = static_cast<const E *>(a.xbc) + b * a.T * a.ldx + c0;
+    const uint32_t mine = (uint32_t)__cvta_generic_to_shared(&ring[0][threadIdx.x]);
+    const auto fetch = [&](int t, int stage) {  // tokens t .. t + kGroup - 1 of the strip
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u)
+            if (t + u < t1)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                 mine + (stage * kGroup + u) * (kThreads * 16)),
+                             "l"(in + (t + u) * a.ldx)
+                             : "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s)
+        fetch(t0 + s * kGroup, s);
+
+    float w[W][VEC], bias[VEC], win[W - 1][VEC];
+    load_weights<E, VEC, W>(a, c0, w);
+    Chunk<E, VEC> rb;
+    if (a.bias)
+        rb = load_chunk<E, VEC>(a.bias, c0);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+        bias[e] = a.bias ? widen<E>(rb.v[e]) : 0.f;
+    const int64_t tap_at = (int64_t)slot * a.cslot + (int64_t)c0 * a.cc;
+    if (strip == 0) {
+        E old[W - 1][VEC];
+        load_taps<E, VEC, W>(a, tap_at, old);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                win[j][e] = widen<E>(old[j][e]);
+        // the window's new taps: the last W-1 of (old taps, tokens)
+        if (a.update) {
+            E nw[W - 1][VEC];
+            new_taps<E, VEC, W>(old, nw, L, [&](int t) {
+                return load_chunk<E, VEC>(in, t * a.ldx);
+            });
+            store_taps<E, VEC, W>(a, tap_at, nw);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+            widen_chunk<E, VEC>(load_chunk<E, VEC>(in, (t0 - (W - 1) + j) * a.ldx), win[j]);
+    }
+
+    int stage = 0;
+    for (int t = t0; t < t1; t += kGroup) {
+        fetch(t + (kStages - 1) * kGroup, stage == 0 ? kStages - 1 : stage - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u) {
+            if (t + u < t1) {
+                float f[VEC], acc[VEC];
+                widen_chunk<E, VEC>(ring[stage * kGroup + u][threadIdx.x], f);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    acc[e] = bias[e];
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k)
+                    fma_vec<VEC>(acc, w[k], win[k]);
+                fma_vec<VEC>(acc, w[W - 1], f);
+                if (a.silu)
+                    silu_vec<E, VEC>(acc);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+                    for (int k = 0; k + 1 < W - 1; ++k)
+                        win[k][e] = win[k + 1][e];
+                    win[W - 2][e] = f[e];
+                }
+                store_floats<E, VEC>(out.p + (t + u) * out.ld, acc);
+            }
+        }
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Every other width (1, 5..16): a thread per (row, strip, channel) that reads each tap
@@ -596,10 +741,13 @@ conv_tree_kernel(const __grid_constant__ ConvPrefillArgs a, const int blocks, co
                 add(k, w[0]);
             }
         }
-        const bool bad = s_bad[t];
+        if (a.silu)
+            silu_vec<E, V>(acc);
+        if (s_bad[t]) {
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-            acc[e] = bad ? 0.f : (a.silu ? conv_silu<E>(acc[e]) : acc[e]);
+            for (int e = 0; e < V; ++e)
+                acc[e] = 0.f;
+        }
         store(t, acc);
     }
 }
@@ -645,23 +793,9 @@ conv_replay_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups, 
         E old[W - 1][VEC], nw[W - 1][VEC];
         if (k < W - 1)
             load_taps<E, VEC, W>(a, tap_at, old);
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j) {
-            const int t = k + j - (W - 1);
-            if (t >= 0) {
-                const Chunk<E, VEC> c = load_chunk<E, VEC>(in, (ids ? ids[t] : t) * a.ldx);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    nw[j][e] = c.v[e];
-            } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-#pragma unroll
-                    for (int o = 0; o < W - 1; ++o)
-                        if (o == k + j)
-                            nw[j][e] = old[o][e];
-            }
-        }
+        new_taps<E, VEC, W>(old, nw, k, [&](int t) {
+            return load_chunk<E, VEC>(in, (ids ? ids[t] : t) * a.ldx);
+        });
         store_taps<E, VEC, W>(a, tap_at, nw);
     } else {
         E *tap = static_cast<E *>(a.cstate) + tap_at;
@@ -709,8 +843,23 @@ int launch_w(const ConvPrefillArgs &a, cudaStream_t s)
         return launch_kernel(conv_prefill_any_kernel<E>, (unsigned)blocks, kThreads, 0, s, a, groups,
                              strips);
     else
-        return launch_kernel(conv_prefill_kernel<E, VEC, W>, (unsigned)blocks, kThreads, 0, s, a,
-                             groups, strips);
+        // one token at a time keeps few registers, which is what a single token wants; rows of
+        // single channels load eight ahead
+        return a.T < 8 ? launch_kernel(conv_prefill_kernel<E, VEC, W, 1>, (unsigned)blocks, kThreads, 0,
+                                       s, a, groups, strips)
+                       : launch_kernel(conv_prefill_kernel<E, 1, W, 8>, (unsigned)blocks, kThreads,
+                                       0, s, a, groups, strips);
+}
+
+template <typename E, int W> int launch_stream(const ConvPrefillArgs &a, cudaStream_t s)
+{
+    const int groups = (a.x_dim + 2 * a.bc_dim) / Vec16<E>::kElems;
+    const int strips = (a.T + kStrip - 1) / kStrip;
+    const int64_t blocks = ((int64_t)groups * strips * a.active + kThreads - 1) / kThreads;
+    if (blocks > 0x7fffffffLL)
+        return SSU_ERR_SHAPE;
+    return launch_kernel(conv_stream_kernel<E, W>, (unsigned)blocks, kThreads, 0, s, a, groups,
+                         strips);
 }
 
 template <typename E, int W> int launch_tree(const ConvPrefillArgs &a, bool vec, cudaStream_t s)
@@ -748,7 +897,15 @@ template <typename E> int launch_e(ConvPrefillArgs a, cudaStream_t s)
     if (!vec)
         return launch_v<E, 1>(a, s);
     a.win_mode = window_mode<E>(a);
-    return launch_v<E, Vec16<E>::kElems / HALF>(a, s);
+    if (a.T >= 8) {
+        switch (a.width) {
+        case 2: return launch_stream<E, 2>(a, s);
+        case 3: return launch_stream<E, 3>(a, s);
+        case 4: return launch_stream<E, 4>(a, s);
+        }
+    }
+    // half vectors: fewer registers a thread and twice the threads for the few tokens
+    return launch_v<E, Vec16<E>::kElems / 2>(a, s);
 }
 
 template <typename E, int VEC, int W>

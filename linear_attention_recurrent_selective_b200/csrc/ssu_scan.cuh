@@ -2,7 +2,7 @@
 // ssu_scan_decode.cu).
 #pragma once
 
-#include "ssu_common.cuh"
+#include "ssu_math.cuh"
 
 namespace ssu {
 namespace scan {
@@ -13,26 +13,6 @@ template <int N> struct Geo {
     static constexpr int kLanes = N / kStates;          // 2, 4, 8, 16, 32, 32
     static constexpr int kPerWarp = 32 / kLanes;        // channels of a warp
 };
-
-// 2^v by the special-function unit (relative error about 2^-22.5); 2^-inf = 0.
-__device__ __forceinline__ float exp2_fast(float v)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-
-__device__ __forceinline__ float rcp_fast(float v)
-{
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
 
 // log(1 + e^v) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1], for two values. With
 // s = e / (2 + e) <= 1/3, log1p(e) = 2 atanh(s) = 2 s (1 + s^2/3 + s^4/5 + ...), here with
@@ -58,17 +38,10 @@ __device__ __forceinline__ float2 softplus2(float2 v)
     return fma2(add2(s, s), p, make_float2(v.x < 0.f ? 0.f : v.x, v.y < 0.f ? 0.f : v.y));
 }
 
-// silu of two values, with the approximate exponential and reciprocal: relative error below
-// 2^-20 for |z| < 20, which a 16-bit output's rounding (2^-9 or 2^-11) hides; fp32 outputs
-// take the accurate one. (Far below zero the reciprocal of 2^127 and more is 0, and so is
-// the gate.)
+// silu of two gate values, for outputs of type `out_dtype`.
 __device__ __forceinline__ float2 gate2(float2 z, int out_dtype)
 {
-    if (out_dtype == SSU_F32)
-        return make_float2(silu_f(z.x), silu_f(z.y));
-    const float2 m = mul2(z, both(-1.44269504f));
-    const float2 e = add2(make_float2(exp2_fast(m.x), exp2_fast(m.y)), both(1.f));
-    return mul2(z, make_float2(rcp_fast(e.x), rcp_fast(e.y)));
+    return out_dtype == SSU_F32 ? silu2<true>(z) : silu2<false>(z);
 }
 
 // The lanes of a channel share out four items (tokens of a prompt, rows of a batch): a lane

@@ -19,9 +19,10 @@
 // for one: a few dependent loads find the row, then it is streamed once.
 //
 // Layout: a cluster of CTAs per sequence. Every CTA walks the chain or tree itself (a few
-// gathers), then each warp sums one contiguous region of the row; the CTAs exchange their
-// sums through distributed shared memory (one cluster barrier), every CTA finds the region
-// that holds the border, and the warp that owns it scans it again from L2.
+// gathers), then each warp sums one contiguous region of the row in kChunks chunks, whose
+// lane sums stay in shared memory; the CTAs exchange their sums through distributed shared
+// memory (one cluster barrier) and every CTA finds the region that holds the border. The
+// warp that owns it finds the chunk from the lane sums and scans only that again (from L2).
 #include <cooperative_groups.h>
 
 #include "ssu_common.cuh"
@@ -31,9 +32,11 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kFill = 592;            // CTAs that give 148 SMs four each
+constexpr int kChunks = 16;           // of a warp's region
 constexpr int kMaxTree = 128;         // nodes of a tree (the verify budget of ssu_ddtree)
 
 template <typename E> __device__ __forceinline__ float to_f32(E v);
@@ -53,164 +56,336 @@ struct Shared {
     int ndrop, stop, root, n, end;
     double warp_sum[kWarps];
     double cta_sum[2][kMaxCluster];   // one set per attempt
+    double lane_sum[kWarps][kChunks][32];
 };
 
-// The row a token is drawn from, and what of it carries mass.
+// The row a token is drawn from, and what of it carries mass. Elements are numbered from
+// -first >= 0 on, so that element 0 modulo VEC starts on 16 bytes.
 template <typename E> struct Row {
-    const E *p, *q;                   // q: subtracted where present
+    const E *p, *q;                   // element 0; q: subtracted (read with kQ only)
     const int *drop;
-    int ndrop, V;
-
-    __device__ __forceinline__ double mass(int i, float pv, float qv) const
-    {
-        const float a = mass_of(pv), b = mass_of(qv);
-        // the difference of two floats in double: exact unless they are 2^29 apart
-        return a > b ? (double)a - (double)b : 0.0;
-    }
+    int ndrop, first, end;            // elements [-first, end) exist: token = first + element
 };
 
-// VEC neighbouring masses from element i (elements at or beyond `end` have none).
-// `dropped`: some dropped token lies among them.
-template <typename E, int VEC>
-__device__ __forceinline__ void masses(const Row<E> &r, int i, int end, const float (&pv)[VEC],
-                                       const float (&qv)[VEC], bool dropped, double (&m)[VEC])
+// VEC neighbouring elements as raw bits: one access, or with kEdge those of [lo, hi) one by
+// one and zeros beyond.
+template <typename E, int VEC, bool kEdge>
+__device__ __forceinline__ void load_probs(const E *p, int i, int lo, int hi, uint32_t (&w)[4])
 {
+    if constexpr (VEC > 1 && !kEdge) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p + i);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (VEC > 1) {
+        E e[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)
+            e[k] = i + k >= lo && i + k < hi ? p[i + k] : E(0.f);
+        memcpy(w, e, 16);
+    } else {
+        w[0] = !kEdge || (i >= lo && i < hi) ? __float_as_uint(to_f32<E>(p[i])) : 0u;
+    }
+}
+
+template <typename E, int VEC>
+__device__ __forceinline__ void unpack_probs(const uint32_t (&w)[4], float (&f)[VEC])
+{
+    if constexpr (VEC > 1)
+        Vec16<E>::unpack(make_uint4(w[0], w[1], w[2], w[3]), f);
+    else
+        f[0] = __uint_as_float(w[0]);
+}
+
+// The masses of VEC neighbouring elements from i on. `dropped`: some of the dropped tokens
+// may be among them.
+template <typename E, int VEC, bool kQ>
+__device__ __forceinline__ void masses(const Row<E> &r, int i, const uint32_t (&pw)[4],
+                                       const uint32_t (&qw)[4], bool dropped, double (&m)[VEC])
+{
+    float pv[VEC], qv[VEC];
+    unpack_probs<E, VEC>(pw, pv);
+    if (kQ)
+        unpack_probs<E, VEC>(qw, qv);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-        m[e] = i + e < end ? r.mass(i + e, pv[e], qv[e]) : 0.0;
-        if (dropped)
-            for (int k = 0; k < r.ndrop; ++k)
-                if (r.drop[k] == i + e)
+        m[e] = (double)mass_of(pv[e]);
+        // the difference of two floats in double: exact unless they are 2^29 apart
+        if (kQ)
+            m[e] = fmax(m[e] - (double)mass_of(qv[e]), 0.0);
+    }
+    if (dropped) {
+        for (int k = 0; k < r.ndrop; ++k)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (r.drop[k] - r.first == i + e)
                     m[e] = 0.0;
     }
 }
 
-template <typename E, int VEC>
-__device__ __forceinline__ void load_probs(const E *p, int i, int end, float (&f)[VEC])
+template <int VEC> __device__ __forceinline__ double sum_of(const double (&m)[VEC])
 {
-    if constexpr (VEC > 1) {
-        if (i + VEC <= end) {
-            Vec16<E>::unpack(*reinterpret_cast<const uint4 *>(p + i), f);
-            return;
-        }
-    }
+    double s[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e)
-        f[e] = i + e < end ? to_f32<E>(p[i + e]) : 0.f;
+        s[e] = m[e];
+#pragma unroll
+    for (int d = VEC / 2; d > 0; d /= 2)
+#pragma unroll
+        for (int e = 0; e < d; ++e)
+            s[e] += s[e + d];
+    return s[0];
 }
 
-// Whether a dropped token lies in [lo, hi); the same answer in every lane.
+// Whether a dropped token lies in elements [lo, hi); the same answer in every lane.
 template <typename E>
 __device__ __forceinline__ bool any_dropped(const Row<E> &r, int lo, int hi, int lane)
 {
     bool any = false;
     for (int k = lane; k < r.ndrop; k += 32)
-        any |= r.drop[k] >= lo && r.drop[k] < hi;
+        any |= r.drop[k] - r.first >= lo && r.drop[k] - r.first < hi;
     return __any_sync(~0u, any);
 }
 
-// The sum of the masses of [lo, hi), in every lane.
-template <typename E, int VEC>
-__device__ double region_sum(const Row<E> &r, int lo, int hi, int lane)
+// Sums of the masses of [lo, hi) by lane for every chunk of `per` elements (a multiple of
+// 32 VEC), into out[chunk][lane]; returns the whole sum, in every lane.
+template <typename E, int VEC, bool kQ>
+__device__ __forceinline__ double region_sum(const Row<E> &r, int lo, int hi, int per, int lane,
+                                             double (*out)[32])
 {
-    constexpr int kStep = 32 * VEC, kUnroll = 4;
+    constexpr int kStep = 32 * VEC, kUnroll = VEC == 1 ? 8 : 16 / VEC;
     const bool dropped = any_dropped(r, lo, hi, lane);
-    double sum = 0.0;
-    for (int i0 = lo; i0 < hi; i0 += kStep * kUnroll) {
-        float pv[kUnroll][VEC], qv[kUnroll][VEC];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int i = i0 + u * kStep + lane * VEC;
-            load_probs<E, VEC>(r.p, i, hi, pv[u]);
-            if (r.q) {
-                load_probs<E, VEC>(r.q, i, hi, qv[u]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    qv[u][e] = 0.f;
-            }
+    const int from = -r.first, to = min(hi, r.end);
+    double all = 0.0, sum = 0.0;
+    int chunk = 0, next = lo + per;                 // end of the current chunk
+    uint32_t pw[kUnroll][4], qw[kUnroll][4];
+    const auto step = [&](int at, const uint32_t (&p)[4], const uint32_t (&q)[4]) {
+        double m[VEC];
+        masses<E, VEC, kQ>(r, at + lane * VEC, p, q, dropped, m);
+        sum += sum_of<VEC>(m);
+        if (at + kStep == next || at + kStep >= hi) {
+            out[chunk++][lane] = sum;
+            all += sum;
+            sum = 0.0;
+            next += per;
         }
+    };
+    int at = lo;
+    while (at < hi) {
+        if (at >= from && at + kStep * kUnroll <= to) {     // a batch of whole steps
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            double m[VEC];
-            masses<E, VEC>(r, i0 + u * kStep + lane * VEC, hi, pv[u], qv[u], dropped, m);
+            for (int u = 0; u < kUnroll; ++u) {
+                load_probs<E, VEC, false>(r.p, at + u * kStep + lane * VEC, from, to, pw[u]);
+                if (kQ)
+                    load_probs<E, VEC, false>(r.q, at + u * kStep + lane * VEC, from, to, qw[u]);
+            }
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                sum += m[e];
+            for (int u = 0; u < kUnroll; ++u)
+                step(at + u * kStep, pw[u], qw[u]);
+            at += kStep * kUnroll;
+        } else {                                            // a step at the row's ends
+            load_probs<E, VEC, true>(r.p, at + lane * VEC, from, to, pw[0]);
+            if (kQ)
+                load_probs<E, VEC, true>(r.q, at + lane * VEC, from, to, qw[0]);
+            step(at, pw[0], qw[0]);
+            at += kStep;
         }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
-        sum += __shfl_xor_sync(~0u, sum, o);
-    return sum;
+        all += __shfl_xor_sync(~0u, all, o);
+    return all;
 }
 
-// The first token of [lo, hi) with mass at which `before` plus the running sum exceeds thr;
-// the region's last token with mass where rounding leaves none.
-template <typename E, int VEC>
-__device__ int region_find(const Row<E> &r, int lo, int hi, double before, double thr, int lane)
+// An inclusive running sum over the lanes.
+__device__ __forceinline__ double running(double v, int lane)
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double up = __shfl_up_sync(~0u, v, o);
+        v += lane >= o ? up : 0.0;
+    }
+    return v;
+}
+
+// The token at the first element of [lo, hi) with mass at which `before` plus the running
+// sum exceeds thr; the last one with mass where rounding leaves none.
+template <typename E, int VEC, bool kQ>
+__device__ __noinline__ int find_in(const Row<E> r, int lo, int hi, double before, double thr,
+                                    int lane)
 {
     const bool dropped = any_dropped(r, lo, hi, lane);
+    const int from = -r.first, to = min(hi, r.end);
     int last = -1;
     for (int i0 = lo; i0 < hi; i0 += 32 * VEC) {
         const int i = i0 + lane * VEC;
-        float pv[VEC], qv[VEC];
-        load_probs<E, VEC>(r.p, i, hi, pv);
-        if (r.q) {
-            load_probs<E, VEC>(r.q, i, hi, qv);
-        } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                qv[e] = 0.f;
-        }
-        double m[VEC], mine = 0.0;
-        masses<E, VEC>(r, i, hi, pv, qv, dropped, m);
+        uint32_t pw[4], qw[4];
+        load_probs<E, VEC, true>(r.p, i, from, to, pw);
+        if (kQ)
+            load_probs<E, VEC, true>(r.q, i, from, to, qw);
+        double m[VEC];
+        masses<E, VEC, kQ>(r, i, pw, qw, dropped, m);
+        const double mine = sum_of<VEC>(m);
         int tail = -1;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            mine += m[e];
+        for (int e = 0; e < VEC; ++e)
             tail = m[e] > 0.0 ? i + e : tail;
-        }
-        double incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double up = __shfl_up_sync(~0u, incl, o);
-            incl += lane >= o ? up : 0.0;
-        }
+        const double incl = running(mine, lane);
         const unsigned hit = __ballot_sync(~0u, mine > 0.0 && before + incl > thr);
+        double run = __shfl_up_sync(~0u, incl, 1);
+        run = before + (lane ? run : 0.0);
         if (hit) {
-            const int src = __ffs(hit) - 1;
-            double run = __shfl_up_sync(~0u, incl, 1);
-            run = before + (lane ? run : 0.0);
-            int at = tail;
+            int at = -1;
 #pragma unroll
-            for (int e = VEC - 1; e >= 0; --e) {     // backwards: the first hit stays
-                double upto = run;
-#pragma unroll
-                for (int f = 0; f <= e; ++f)
-                    upto += m[f];
-                if (m[e] > 0.0 && upto > thr)
+            for (int e = 0; e < VEC; ++e) {
+                run += m[e];
+                if (m[e] > 0.0 && (run > thr || i + e == tail) && at < 0)
                     at = i + e;
             }
-            return __shfl_sync(~0u, at, src);
+            return r.first + __shfl_sync(~0u, at, __ffs(hit) - 1);
         }
         before += __shfl_sync(~0u, incl, 31);
         const unsigned some = __ballot_sync(~0u, tail >= 0);
         if (some)
             last = __shfl_sync(~0u, tail, 31 - __clz(some));
     }
-    return last;
+    return r.first + last;
 }
 
+// The same over a warp's whole region, from its lane sums: the chunk first.
+template <typename E, int VEC, bool kQ>
+__device__ __forceinline__ int region_find(const Row<E> &r, int lo, int hi, int per, double before,
+                                           double thr, int lane, const double (*sums)[32])
+{
+    static_assert(kChunks == 16, "two lanes a chunk");
+    const int chunks = (hi - lo + per - 1) / per, c = lane >> 1;
+    double part[4] = {};
+    if (c < chunks)
+#pragma unroll
+        for (int k = 0; k < 16; ++k)                // (rotated: lanes on different banks)
+            part[k & 3] += sums[c][(lane & 1) * 16 + ((k + lane) & 15)];
+    double mine = sum_of<4>(part);
+    mine += __shfl_xor_sync(~0u, mine, 1);          // the chunk's sum, in both of its lanes
+    const bool odd = lane & 1;
+    const double incl = running(odd ? mine : 0.0, lane);    // odd lanes: up to their chunk
+    const unsigned some = __ballot_sync(~0u, odd && mine > 0.0);
+    const unsigned hit = __ballot_sync(~0u, odd && mine > 0.0 && before + incl > thr);
+    // (some is not empty: the region's sum is positive)
+    const int at = hit ? __ffs(hit) - 1 : 31 - __clz(some);
+    const double upto = __shfl_sync(~0u, incl - mine, at);
+    const int from = lo + (at >> 1) * per;
+    const double inf = __longlong_as_double(0x7ff0000000000000LL);
+    return find_in<E, VEC, kQ>(r, from, min(from + per, hi), before + upto, hit ? thr : inf, lane);
+}
+
+// Draw row b's next token from the masses of `row` (less `sub`, without the dropped tokens),
+// whose element 0 lies `skew` elements behind a 16-byte boundary.
 template <typename E, int VEC>
-__global__ void __launch_bounds__(kThreads)
+__device__ __forceinline__ void draw(const VerifyArgs &a, Shared &s, cg::cluster_group &cluster,
+                                     int b, const E *row, const E *sub, int skew, float us)
+{
+    const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    Row<E> r;
+    r.first = -skew;
+    r.end = a.V + skew;
+    r.p = row - skew;
+    r.q = sub ? sub - skew : nullptr;
+    r.drop = s.drop;
+    r.ndrop = s.ndrop;
+    // warps take contiguous regions of at most kChunks chunks of `per` elements
+    constexpr int kStep = 32 * VEC;
+    const int regions = C * kWarps;
+    const int steps = ((r.end + regions - 1) / regions + kStep - 1) / kStep;
+    const int per = (steps + kChunks - 1) / kChunks * kStep;
+    const int64_t lo64 = (int64_t)(rank * kWarps + warp) * steps * kStep;
+    const int lo = (int)min(lo64, (int64_t)r.end);
+    const int hi = (int)min(lo64 + (int64_t)steps * kStep, (int64_t)r.end);
+
+    // A residual without mass (p <= q wherever p has any, or a rejected token that held it
+    // all) can only come from rounding: the draw is then from p itself.
+    for (int attempt = 0; attempt < 2; ++attempt) {
+        const double mine = r.q ? region_sum<E, VEC, true>(r, lo, hi, per, lane, s.lane_sum[warp])
+                                : region_sum<E, VEC, false>(r, lo, hi, per, lane, s.lane_sum[warp]);
+        if (lane == 0)
+            s.warp_sum[warp] = mine;
+        __syncthreads();
+        if (tid < C) {
+            double sum = 0.0;
+            for (int w = 0; w < kWarps; ++w)
+                sum += s.warp_sum[w];
+            *cluster.map_shared_rank(&s.cta_sum[attempt][rank], tid) = sum;
+        }
+        cluster.sync();
+        double total = 0.0;
+        for (int c = 0; c < C; ++c)
+            total += s.cta_sum[attempt][c];
+        if (total > 0.0) {
+            // the CTA, then its warp, whose running sum first exceeds thr (sums of
+            // non-negative numbers in one order never decrease); the last one with any
+            // mass where none does
+            const double thr = (double)us * total;
+            int owner = -1, last = -1;
+            double run = 0.0, before = 0.0;
+            for (int c = 0; c < C; ++c) {
+                const double v = s.cta_sum[attempt][c];
+                if (v > 0.0) {
+                    last = c;
+                    if (owner < 0 && run + v > thr) {
+                        owner = c;
+                        before = run;
+                    }
+                }
+                run += v;
+            }
+            const bool beyond = owner < 0;
+            if (rank != (beyond ? last : owner))
+                return;
+            int w_owner = -1, w_last = -1;
+            double w_run = before, w_before = 0.0;
+            for (int w = 0; w < kWarps; ++w) {
+                const double v = s.warp_sum[w];
+                if (v > 0.0) {
+                    w_last = w;
+                    if (!beyond && w_owner < 0 && w_run + v > thr) {
+                        w_owner = w;
+                        w_before = w_run;
+                    }
+                }
+                w_run += v;
+            }
+            const bool tail = w_owner < 0;
+            if (warp == (tail ? w_last : w_owner)) {
+                __syncwarp();
+                const double inf = __longlong_as_double(0x7ff0000000000000LL);
+                const double t = tail ? inf : thr;
+                const int at = r.q ? region_find<E, VEC, true>(r, lo, hi, per, w_before, t, lane,
+                                                               s.lane_sum[warp])
+                                   : region_find<E, VEC, false>(r, lo, hi, per, w_before, t, lane,
+                                                                s.lane_sum[warp]);
+                if (lane == 0)
+                    a.next[b] = at;
+            }
+            return;
+        }
+        r.q = nullptr;
+        r.ndrop = 0;
+        __syncthreads();                        // the sums are written again
+    }
+    if (rank == 0 && tid == 0) {                // no mass at all
+        a.next[b] = -1;
+        if (a.err)
+            atomicOr(a.err, SSU_FLAG_NO_MASS);
+    }
+}
+
+template <typename E>
+__global__ void __launch_bounds__(kThreads, 4)
 verify_kernel(const __grid_constant__ VerifyArgs a)
 {
     __shared__ Shared s;
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int b = blockIdx.x / C;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x;
     const bool report = rank == 0 && a.err;
     cluster.barrier_arrive();         // waited for before another CTA's memory is written
 
@@ -333,126 +508,40 @@ verify_kernel(const __grid_constant__ VerifyArgs a)
     if (n == 0)                                 // the same in every CTA of the cluster
         return;
 
-    // ---- the next token
+    // ---- the next token, by whole vectors where both rows allow it
+    constexpr int V = Vec16<E>::kElems;
     const bool rejected = !a.parents && n < L;
-    Row<E> r;
-    r.p = rows + s.end * a.ldp;
-    r.q = rejected && drafts ? drafts + s.end * a.ldq : nullptr;
-    r.drop = s.drop;
-    r.ndrop = s.ndrop;
-    r.V = a.V;
-    constexpr int kStep = 32 * VEC;
-    const int regions = C * kWarps;
-    const int len = ((a.V + regions - 1) / regions + kStep - 1) / kStep * kStep;
-    const int64_t lo64 = (int64_t)(rank * kWarps + warp) * len;
-    const int lo = (int)min(lo64, (int64_t)a.V), hi = (int)min(lo64 + len, (int64_t)a.V);
-
-    // A residual without mass (p <= q wherever p has any, or a rejected token that held it
-    // all) can only come from rounding: the draw is then from p itself.
-    for (int attempt = 0; attempt < 2; ++attempt) {
-        const double mine = region_sum<E, VEC>(r, lo, hi, lane);
-        if (lane == 0)
-            s.warp_sum[warp] = mine;
-        __syncthreads();
-        if (tid < C) {
-            double sum = 0.0;
-            for (int w = 0; w < kWarps; ++w)
-                sum += s.warp_sum[w];
-            *cluster.map_shared_rank(&s.cta_sum[attempt][rank], tid) = sum;
-        }
-        cluster.sync();
-        double total = 0.0;
-        for (int c = 0; c < C; ++c)
-            total += s.cta_sum[attempt][c];
-        if (total > 0.0) {
-            // the CTA, then its warp, whose running sum first exceeds thr (sums of
-            // non-negative numbers in one order never decrease); the last one with any
-            // mass where none does
-            const double thr = (double)us * total;
-            int owner = -1, last = -1;
-            double run = 0.0, before = 0.0;
-            for (int c = 0; c < C; ++c) {
-                const double v = s.cta_sum[attempt][c];
-                if (v > 0.0) {
-                    last = c;
-                    if (owner < 0 && run + v > thr) {
-                        owner = c;
-                        before = run;
-                    }
-                }
-                run += v;
-            }
-            const bool beyond = owner < 0;
-            if (beyond)
-                owner = last;
-            if (rank != owner)
-                return;
-            int w_owner = -1, w_last = -1;
-            double w_run = before, w_before = 0.0;
-            for (int w = 0; w < kWarps; ++w) {
-                const double v = s.warp_sum[w];
-                if (v > 0.0) {
-                    w_last = w;
-                    if (!beyond && w_owner < 0 && w_run + v > thr) {
-                        w_owner = w;
-                        w_before = w_run;
-                    }
-                }
-                w_run += v;
-            }
-            const bool tail = w_owner < 0;
-            if (tail)
-                w_owner = w_last;
-            if (warp == w_owner) {
-                const double inf = __longlong_as_double(0x7ff0000000000000LL);
-                const int at = region_find<E, VEC>(r, lo, hi, w_before, tail ? inf : thr, lane);
-                if (lane == 0)
-                    a.next[b] = at;
-            }
-            return;
-        }
-        r.q = nullptr;
-        r.ndrop = 0;
-        __syncthreads();                        // warp_sum is written again
-    }
-    if (rank == 0 && tid == 0) {                // no mass at all
-        a.next[b] = -1;
-        if (a.err)
-            atomicOr(a.err, SSU_FLAG_NO_MASS);
-    }
+    const E *const row = rows + s.end * a.ldp;
+    const E *const sub = rejected && drafts ? drafts + s.end * a.ldq : nullptr;
+    const int skew = (int)(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(E));
+    if (!sub || (int)(reinterpret_cast<uintptr_t>(sub) % 16 / sizeof(E)) == skew)
+        draw<E, V>(a, s, cluster, b, row, sub, skew, us);
+    else
+        draw<E, 1>(a, s, cluster, b, row, sub, 0, us);
 }
 
-template <typename E, int VEC> int launch_v(const VerifyArgs &a, cudaStream_t s)
+template <typename E> int launch_e(const VerifyArgs &a, cudaStream_t s)
 {
-    // CTAs of a sequence: as many as fill the card once, and no more than leave each warp
-    // one step of 32 vectors
+    // CTAs of a sequence: as many as the card holds at once (four an SM), and no more than
+    // leave each warp one step of 32 vectors
     int c = 1;
-    while (c < kMaxCluster && (int64_t)a.active * c < 296 && a.V > c * kWarps * 32 * VEC)
+    while (c < kMaxCluster && (int64_t)a.active * c * 2 <= kFill &&
+           a.V > c * kWarps * 32 * Vec16<E>::kElems)
         c *= 2;
+    if ((int64_t)a.active * c > 0x7fffffffLL)
+        return SSU_ERR_SHAPE;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = c;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    if ((int64_t)a.active * c > 0x7fffffffLL)
-        return SSU_ERR_SHAPE;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.active * c));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, verify_kernel<E, VEC>, a) == cudaSuccess ? SSU_OK
-                                                                             : SSU_ERR_CUDA;
-}
-
-template <typename E> int launch_e(const VerifyArgs &a, cudaStream_t s)
-{
-    constexpr int V = Vec16<E>::kElems;
-    const auto ok = [](const void *p, int64_t ld) {
-        return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % V == 0;
-    };
-    return ok(a.p, a.ldp) && (!a.q || ok(a.q, a.ldq)) ? launch_v<E, V>(a, s) : launch_v<E, 1>(a, s);
+    return cudaLaunchKernelEx(&cfg, verify_kernel<E>, a) == cudaSuccess ? SSU_OK : SSU_ERR_CUDA;
 }
 
 }  // namespace
