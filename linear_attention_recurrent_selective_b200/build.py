@@ -4,6 +4,9 @@ Usage: python -m linear_attention_recurrent_selective_b200.build [--force] [--ve
 Objects go to _build/ at the repository root; the shared library lands next to this
 file so that it travels with the package.
 
+The Python binding's native argument marshalling (csrc/marshal.cpp, a CPython module that
+reads torch tensors) is built beside it as _marshal.so with the C++ compiler.
+
 The same sources also build libssu_waittest.so (objects in _build/waittest/), with
 SSU_WAIT_TEST defined: the test suite's library in which a chosen bounded wait can be
 made to run out (include/ssu_wait_test.h). Nothing but the tests loads it.
@@ -18,6 +21,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,6 +29,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libssu.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 WAITTEST_LIB = os.path.join(PKG, "libssu_waittest.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -55,9 +60,36 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps() + [__file__])
 
 
+def build_marshal(force: bool = False) -> str:
+    """Build _marshal.so, the binding's native argument marshalling."""
+    src = os.path.join(CSRC, "marshal.cpp")
+    deps = [src, __file__] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(MARSHAL) and \
+            all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in deps):
+        return MARSHAL
+    import torch
+    home = os.path.dirname(torch.__file__)
+    inc, libs = os.path.join(home, "include"), os.path.join(home, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    tmp = MARSHAL + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, src, "-o", tmp,
+           "-L", libs, f"-Wl,-rpath,{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False, waittest: bool = False) -> str:
-    """Build libssu.so (or, with waittest, the test library libssu_waittest.so)."""
+    """Build libssu.so and _marshal.so (or, with waittest, the test library
+    libssu_waittest.so)."""
     lib = WAITTEST_LIB if waittest else LIB
+    if not waittest:
+        build_marshal(force)
     if not force and up_to_date(lib):
         return lib
     objdir = os.path.join(BUILD, "waittest") if waittest else BUILD

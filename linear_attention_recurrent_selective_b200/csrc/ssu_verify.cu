@@ -107,10 +107,12 @@ __device__ __forceinline__ void masses(const Row<E> &r, int i, const uint32_t (&
         unpack_probs<E, VEC>(qw, qv);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-        m[e] = (double)mass_of(pv[e]);
-        // the difference of two floats in double: exact unless they are 2^29 apart
-        if (kQ)
-            m[e] = fmax(m[e] - (double)mass_of(qv[e]), 0.0);
+        const float v = mass_of(pv[e]);
+        m[e] = (double)v;
+        if (kQ) {       // max(p - q, 0); the difference is exact unless they are 2^29 apart
+            const float q = mass_of(qv[e]);
+            m[e] -= (double)(v > q ? q : v);
+        }
     }
     if (dropped) {
         for (int k = 0; k < r.ndrop; ++k)

@@ -2,7 +2,8 @@
 
 Argument marshalling only: every function here checks that tensors are CUDA tensors of
 the expected dtype and layout, reads their sizes, and passes raw device pointers and
-the current CUDA stream to the C entry point of the same name. All arithmetic runs in
+the current CUDA stream to the C entry point of the same name (by ctypes, or natively by
+csrc/marshal.cpp for the operators that run for a few microseconds). All arithmetic runs in
 the library's kernels; there is no other implementation to fall back to, and a missing
 library raises ``SSULibraryMissing``.
 
@@ -31,7 +32,6 @@ Semantics (Selective State Update page of the TensorRT-Edge-LLM C++ API):
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 from typing import Optional
 
@@ -355,116 +355,43 @@ def ssu_conv_decode(xbc, conv_weight, conv_state, A, dt, state, out, *, width, c
     return out
 
 
-# The current device and its current stream without building Stream objects (a call's fixed
-# cost counts for launch-bound ones); the public calls where a torch build lacks them.
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-_current_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None) or
-                       (lambda index: torch.cuda.current_stream(index).cuda_stream))
+_native = None
 
 
-def _common_device(*tensors):
-    """Index of the CUDA device that every given tensor lives on (None entries are skipped)."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors on {tensors[0].device} and on {t.device} in one call")
-    if dev < 0:
-        raise ValueError("expected CUDA tensors")
-    return dev
-
-
-def _run(fn, device, stream, *args):
-    """Call the C entry point ``fn`` on ``stream`` (the current one of the tensors' device
-    when None), with that device current for the launch."""
-    f = getattr(_lib or lib(), fn)
-    if stream is None:
-        raw = _current_raw_stream(device)
-    else:
-        raw = stream.cuda_stream
-        if stream.device.index != device:
-            raise ValueError(f"stream of {stream.device} given for tensors on cuda:{device}")
-    if _current_device() == device:
-        rc = f(*args, raw)
-    else:
-        with torch.cuda.device(device):
-            rc = f(*args, raw)
+def _call(name, stream, *args):
+    """Call the entry point ``name`` through the native marshalling (csrc/marshal.cpp), which
+    checks and reads the tensors; raises on an error status."""
+    global _native
+    if _native is None:
+        _native = _load_marshal()
+    L = _lib or lib()
+    try:
+        address = L.addresses[name]
+    except AttributeError:
+        L.addresses = {f: ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in ENTRY_POINTS}
+        address = L.addresses[name]
+    rc = getattr(_native, name)(address, stream, *args)
     if rc:
-        _check(fn, rc)
+        _check(name, rc)
 
 
-def _vector(t, name, n, dtype=torch.int32):
-    """Pointer of a dense [n] tensor of ``dtype`` (None stays NULL)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a dense [{n}] tensor of {dtype}, got "
-                         f"{list(t.shape)} of {t.dtype}")
-    return t.data_ptr()
+def _load_marshal():
+    try:
+        from . import _marshal
+    except ImportError as e:
+        raise SSULibraryMissing(
+            f"the binding's _marshal.so is missing or does not load ({e}): build it with "
+            "`python -m linear_attention_recurrent_selective_b200.build`") from e
+    return _marshal
 
 
-def _dense(t, name, shape, dtype):
-    """Pointer of a contiguous tensor of ``shape`` and ``dtype`` (None stays NULL)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {list(shape)} of {dtype}, got "
-                         f"{list(t.shape)} of {t.dtype}")
-    return t.data_ptr()
-
-
-def _tokens(t, name, shape, lead, per):
-    """Elements between consecutive tokens of ``t``, whose ``shape`` is ``lead`` (1: rows, 2:
-    rows and tokens) leading sizes and then those of a token of ``per`` elements: each token
-    is dense, and the tokens of all rows are equally far apart (slices of wider rows)."""
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.is_contiguous():
-        return per
-    step, far = t.stride(), 1
-    for i in range(len(shape) - 1, lead - 1, -1):
-        if shape[i] != 1 and step[i] != far:
-            raise ValueError(f"{name}: a token's elements must be dense")
-        far *= shape[i]
-    if lead == 2 and shape[1] > 1:
-        if shape[0] > 1 and step[0] != shape[1] * step[1]:
-            raise ValueError(f"{name}: rows must follow one another, T tokens apart")
-        return step[1]
-    return step[0] if shape[0] > 1 else far
-
-
-def _extent(t):
-    """Elements of storage from a tensor's first element to its last one."""
-    n = t.numel()
-    if n == 0 or t.is_contiguous():
-        return n
-    return 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
-
-
-def _conv_pool(conv_state, conv_strides, channels, width, dtype, P):
-    """(pointer, slot, channel and tap strides, P) of a conv pool; the tensor must reach
-    over every slot's taps."""
-    if width <= 1 or conv_state is None:
-        return None, 0, 0, 0, (P if P is not None else 2 ** 31 - 1)
-    if conv_state.dtype is not dtype:
-        raise ValueError("conv_state must have xbc's dtype")
-    cs, cc, ck = conv_strides
-    if P is None:
-        P = conv_state.shape[0] if conv_state.dim() == 3 else conv_state.numel() // max(cs, 1)
-    if P > 0:
-        last = (P - 1) * cs + (channels - 1) * cc + (width - 2) * ck
-        if last >= _extent(conv_state):
-            raise ValueError(f"conv_state does not hold {P} slots with strides {conv_strides}")
-    return conv_state.data_ptr(), cs, cc, ck, P
-
-
-def _conv_out(t, name, batch, T, dtype):
-    """(pointer, channels) of an output of the convolution; None has no channels."""
-    if t is None:
-        return None, 0
-    shape = t.shape
-    if t.dtype is not dtype or shape[:2] != (batch, T) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous [batch, T, ...] in xbc's dtype")
-    return t.data_ptr(), shape[2] if len(shape) == 3 else math.prod(shape[2:])
+def _debug_slots(state_indices, pool, P, active, stream):
+    """The debug check of state_indices against a pool's slot count (P, or its first size)."""
+    if _debug_checks and state_indices is not None:
+        if P is None and pool is not None and pool.dim() == 3:
+            P = pool.shape[0]
+        check_state_indices(state_indices, 2 ** 31 - 1 if P is None else P, active_batch=active,
+                            stream=stream)
 
 
 def ssu_conv_prefill(xbc, conv_weight, conv_state, x, B=None, C=None, *, width, conv_strides,
@@ -476,27 +403,13 @@ def ssu_conv_prefill(xbc, conv_weight, conv_state, x, B=None, C=None, *, width, 
     and B, C [batch, T, bc_dim (or G, N)] (None: no such channels). conv_state and
     conv_strides as in ssu_conv_decode. ``update_state`` advances the windows by the row's
     tokens; with ``parent_ids`` [batch, T] the tokens are the nodes of draft trees
-    (update_state must be off: commit with ssu_conv_replay)."""
-    dev = _common_device(xbc, conv_weight, conv_state, x, B, C, conv_bias, state_indices,
-                         context_lengths, parent_ids, err_flags)
-    batch, T, ch = xbc.shape
-    active = batch if active_batch is None else active_batch
-    ld = _tokens(xbc, "xbc", (batch, T, ch), 2, ch)
-    dt = xbc.dtype
-    xp, xd = _conv_out(x, "x", batch, T, dt)
-    Bp, bd = _conv_out(B, "B", batch, T, dt)
-    Cp, cd = _conv_out(C, "C", batch, T, dt)
-    if bd != cd or xd + 2 * bd != ch:
-        raise ValueError(f"x, B and C hold {xd}, {bd} and {cd} channels, xbc {ch}")
-    pool, cs, cc, ck, P = _conv_pool(conv_state, conv_strides, ch, width, dt, P)
-    _debug_indices(state_indices, P, active, stream)
-    _run("ssu_conv_prefill", dev, stream, xbc.data_ptr(), _dt(xbc, "xbc"), ld,
-         _dense(conv_weight, "conv_weight", (ch, width), dt),
-         _vector(conv_bias, "conv_bias", ch, dt), pool, cs, cc, ck, width, int(bool(conv_silu)),
-         P, xp, Bp, Cp, _vector(state_indices, "state_indices", batch),
-         _vector(context_lengths, "context_lengths", batch),
-         _dense(parent_ids, "parent_ids", (batch, T), torch.int32), int(bool(update_state)),
-         batch, active, T, xd, bd, _vector(err_flags, "err_flags", 1))
+    (update_state must be off: commit with ssu_conv_replay). P: slots of the pool (needed
+    unless conv_state is 3-D, or flat with slots that follow one another)."""
+    _debug_slots(state_indices, conv_state, P, active_batch, stream)
+    cs, cc, ck = conv_strides
+    _call("ssu_conv_prefill", stream, xbc, conv_weight, conv_state, x, B, C, conv_bias,
+          state_indices, context_lengths, parent_ids, err_flags, width, cs, cc, ck, conv_silu,
+          update_state, P, active_batch)
     return x, B, C
 
 
@@ -506,61 +419,10 @@ def ssu_conv_replay(xbc, conv_state, accepted_lengths, *, width, conv_strides,
     """Commit the first accepted_lengths[b] tokens of xbc [batch, T, conv_dim] (or the nodes
     accepted_node_ids[b, :accepted_lengths[b]]) to the conv windows, as ssu_replay commits
     them to the recurrent state."""
-    dev = _common_device(xbc, conv_state, accepted_lengths, state_indices, accepted_node_ids,
-                         err_flags)
-    batch, T, ch = xbc.shape
-    active = batch if active_batch is None else active_batch
-    ld = _tokens(xbc, "xbc", (batch, T, ch), 2, ch)
-    pool, cs, cc, ck, P = _conv_pool(conv_state, conv_strides, ch, width, xbc.dtype, P)
-    ids, most = None, 0
-    if accepted_node_ids is not None:
-        if accepted_node_ids.dim() != 2:
-            raise ValueError("accepted_node_ids must be [batch, maxAcceptLen]")
-        most = accepted_node_ids.shape[1]
-        ids = _dense(accepted_node_ids, "accepted_node_ids", (batch, most), torch.int32)
-    _debug_indices(state_indices, P, active, stream)
-    _run("ssu_conv_replay", dev, stream, xbc.data_ptr(), _dt(xbc, "xbc"), ld, pool, cs, cc, ck,
-         width, P, _vector(accepted_lengths, "accepted_lengths", batch),
-         _vector(state_indices, "state_indices", batch), batch, active, T, ch, ids, most,
-         _vector(err_flags, "err_flags", 1))
-
-
-def _scan_args(x, dt, A, B, C, state, out, D, z, dt_bias, state_indices, context_lengths,
-               err_flags, slot_stride, P):
-    """The arguments scan_prefill and scan_decode share, up to state_indices."""
-    dev = _common_device(x, dt, A, B, C, state, out, D, z, dt_bias, state_indices,
-                         context_lengths, err_flags)
-    shape, xdt = x.shape, x.dtype
-    lead, ch = len(shape) - 1, shape[-1]
-    G, N = B.shape[-2:]
-    per, bc = G * N, (*shape[:-1], G, N)
-    if z is not None and z.dtype is not xdt:
-        raise ValueError("z must have x's dtype")
-    if C is not None and C.dtype is not B.dtype:
-        raise ValueError("C must have B's dtype")
-    if state.dim() == 3:
-        size, step = state.shape, state.stride()
-        if size[1:] != (ch, N) or step[1:] != (N, 1):
-            raise ValueError(f"state must be [P, {ch}, {N}], contiguous inside a slot")
-        stride = step[0] if slot_stride is None else slot_stride
-        P = size[0] if P is None else P
-    else:
-        if state.dim() != 1 or not state.is_contiguous():
-            raise ValueError("state must be [P, channels, dstate] or flat contiguous storage")
-        stride = ch * N if slot_stride is None else slot_stride
-        P = state.numel() // max(stride, 1) if P is None else P
-    if P > 0 and (P - 1) * stride + ch * N > _extent(state):
-        raise ValueError(f"state does not hold {P} slots of stride {stride}")
-    f32 = torch.float32
-    return dev, G, N, P, [
-        x.data_ptr(), _dt(x, "x"), _tokens(x, "x", shape, lead, ch), dt.data_ptr(), _dt(dt, "dt"),
-        _tokens(dt, "dt", shape, lead, ch), _dense(A, "A", (ch, N), f32), B.data_ptr(),
-        None if C is None else C.data_ptr(), _dt(B, "B"), _tokens(B, "B", bc, lead, per),
-        per if C is None else _tokens(C, "C", bc, lead, per),
-        _vector(dt_bias, "dt_bias", ch, f32), _vector(D, "D", ch, f32),
-        None if z is None else z.data_ptr(), 0 if z is None else _tokens(z, "z", shape, lead, ch),
-        state.data_ptr(), _dt(state, "state"), stride, P, _dense(out, "out", shape, xdt),
-        _vector(state_indices, "state_indices", shape[0])]
+    _debug_slots(state_indices, conv_state, P, active_batch, stream)
+    cs, cc, ck = conv_strides
+    _call("ssu_conv_replay", stream, xbc, conv_state, accepted_lengths, state_indices,
+          accepted_node_ids, err_flags, width, cs, cc, ck, P, active_batch)
 
 
 def scan_prefill(x, dt, A, B, C, state, out, *, D=None, z=None, dt_bias=None, dt_softplus=True,
@@ -571,14 +433,9 @@ def scan_prefill(x, dt, A, B, C, state, out, *, D=None, z=None, dt_bias=None, dt
     dt_bias, D [channels] fp32; state pool [P, channels, dstate] (or flat with slot_stride).
     x, dt, z, B and C may be slices of wider rows. ``update_state=False`` only reads the pool;
     ``out=None`` only advances it (C may then be None)."""
-    batch, T, ch = x.shape
-    active = batch if active_batch is None else active_batch
-    dev, G, N, P, args = _scan_args(x, dt, A, B, C, state, out, D, z, dt_bias,
-                                    state_indices, context_lengths, err_flags, slot_stride, P)
-    _debug_indices(state_indices, P, active, stream)
-    _run("scan_prefill", dev, stream, *args, _vector(context_lengths, "context_lengths", batch),
-         int(bool(update_state)), batch, active, T, ch, G, N, int(bool(dt_softplus)),
-         _vector(err_flags, "err_flags", 1))
+    _debug_slots(state_indices, state, P, active_batch, stream)
+    _call("scan_prefill", stream, x, dt, A, B, C, state, out, D, z, dt_bias, state_indices,
+          err_flags, dt_softplus, slot_stride, P, active_batch, context_lengths, update_state)
     return out
 
 
@@ -587,13 +444,9 @@ def scan_decode(x, dt, A, B, C, state, out, *, D=None, z=None, dt_bias=None, dt_
                 stream=None):
     """One token of the per-channel selective scan. x, z, out, dt [batch, channels]; B, C
     [batch, G, dstate]; other arguments as in scan_prefill; the state is updated in place."""
-    batch, ch = x.shape
-    active = batch if active_batch is None else active_batch
-    dev, G, N, P, args = _scan_args(x, dt, A, B, C, state, out, D, z, dt_bias,
-                                    state_indices, None, err_flags, slot_stride, P)
-    _debug_indices(state_indices, P, active, stream)
-    _run("scan_decode", dev, stream, *args, batch, active, ch, G, N, int(bool(dt_softplus)),
-         _vector(err_flags, "err_flags", 1))
+    _debug_slots(state_indices, state, P, active_batch, stream)
+    _call("scan_decode", stream, x, dt, A, B, C, state, out, D, z, dt_bias, state_indices,
+          err_flags, dt_softplus, slot_stride, P, active_batch)
     return out
 
 
@@ -607,35 +460,9 @@ def spec_verify(tokens, target_probs, uniforms, uniform_sample, accepted_lengths
     ``parent_ids`` [batch, T] and ``accepted_node_ids`` [batch, maxAcceptLen]. Writes
     accepted_lengths [batch] (for ssu_replay and ssu_conv_replay), next_tokens [batch] and
     accepted_node_ids."""
-    dev = _common_device(tokens, target_probs, uniforms, uniform_sample, accepted_lengths,
-                         next_tokens, draft_probs, parent_ids, accepted_node_ids,
-                         context_lengths, state_indices, err_flags)
-    batch, T, V = target_probs.shape
-    active = batch if active_batch is None else active_batch
-    ldq = 0
-    if draft_probs is not None:
-        if draft_probs.dtype is not target_probs.dtype:
-            raise ValueError("draft_probs must have target_probs' dtype")
-        ldq = _tokens(draft_probs, "draft_probs", (batch, max(T - 1, 0), V), 2, V)
-    i32, f32 = torch.int32, torch.float32
-    most = 0
-    if accepted_node_ids is not None:
-        if accepted_node_ids.dim() != 2:
-            raise ValueError("accepted_node_ids must be [batch, maxAcceptLen]")
-        most = accepted_node_ids.shape[1]
-    _run("spec_verify", dev, stream, _dense(tokens, "tokens", (batch, T), i32),
-         target_probs.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(),
-         _dt(target_probs, "target_probs"),
-         _tokens(target_probs, "target_probs", (batch, T, V), 2, V), ldq,
-         _dense(uniforms, "uniforms", (batch, T), f32),
-         _vector(uniform_sample, "uniform_sample", batch, f32),
-         _vector(context_lengths, "context_lengths", batch),
-         _dense(parent_ids, "parent_ids", (batch, T), i32),
-         _vector(state_indices, "state_indices", batch),
-         _vector(accepted_lengths, "accepted_lengths", batch),
-         _vector(next_tokens, "next_tokens", batch),
-         _dense(accepted_node_ids, "accepted_node_ids", (batch, most), i32), most, batch, active,
-         T, V, _vector(err_flags, "err_flags", 1))
+    _call("spec_verify", stream, tokens, target_probs, uniforms, uniform_sample,
+          accepted_lengths, next_tokens, draft_probs, parent_ids, accepted_node_ids,
+          context_lengths, state_indices, err_flags, active_batch)
     return accepted_lengths, next_tokens
 
 
