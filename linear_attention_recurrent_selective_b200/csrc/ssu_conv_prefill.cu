@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kMaxNodes = 128;        // nodes of a draft tree
+constexpr int kBad = 255;             // in a node's list of rows: it is malformed
 constexpr int kStages = 3, kGroup = 4;  // of a thread's ring
 constexpr int kStrip = 32;            // tokens of a strip, >= the widest window (16) - 1
 
@@ -544,6 +545,86 @@ conv_stream_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups, 
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+// One token a row (T = 1), half vectors: a thread takes the same channels of kRows rows, so
+// that their weights are read once, with every load of both rows issued before the first is
+// used and few enough registers for one wave of 256 rows of 5376 channels. The windows are
+// most of the traffic.
+template <typename E, int VEC, int W>
+__global__ void __launch_bounds__(kThreads, 6)
+conv_token_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups)
+{
+    constexpr int kRows = 2;
+    const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int g = (int)(id % groups), c0 = g * VEC;
+    const int64_t b0 = id / groups * kRows;
+    if (b0 >= a.active)
+        return;
+    int slot[kRows];
+    bool live[kRows];
+    Chunk<E, VEC> x[kRows];
+    E tap[kRows][W - 1][VEC];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        const int64_t b = b0 + r;
+        slot[r] = b < a.active ? (a.idx ? a.idx[b] : (int)b) : a.P;
+        live[r] = slot[r] >= 0 && slot[r] < a.P;
+        if (live[r])
+            live[r] = row_length(a.ctx, (int)b, 1, SSU_FLAG_CONTEXT_RANGE, g == 0, a.err) == 1;
+        else if (b < a.active && slot[r] >= 0 && g == 0 && a.err)
+            atomicOr(a.err, SSU_FLAG_INDEX_RANGE);      // caller bug: skip and report
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+        if (live[r]) {
+            x[r] = load_chunk<E, VEC>(a.xbc, (b0 + r) * a.ldx + c0);
+            load_taps<E, VEC, W>(a, (int64_t)slot[r] * a.cslot + (int64_t)c0 * a.cc, tap[r]);
+        }
+    float w[W][VEC], bias[VEC];
+    load_weights<E, VEC, W>(a, c0, w);
+    Chunk<E, VEC> rb;
+    if (a.bias)
+        rb = load_chunk<E, VEC>(a.bias, c0);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+        bias[e] = a.bias ? widen<E>(rb.v[e]) : 0.f;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        if (!live[r] && slot[r] >= 0)           // past the batch or the pool, or length 0
+            continue;
+        float acc[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            acc[e] = slot[r] < 0 ? 0.f : bias[e];       // padding row: zero
+        if (live[r]) {
+            float f[VEC];
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    f[e] = widen<E>(tap[r][k][e]);
+                fma_vec<VEC>(acc, w[k], f);
+            }
+            widen_chunk<E, VEC>(x[r], f);
+            fma_vec<VEC>(acc, w[W - 1], f);
+            if (a.silu)
+                silu_vec<E, VEC>(acc);
+            if (a.update) {
+                E nw[W - 1][VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+                    for (int k = 0; k + 1 < W - 1; ++k)
+                        nw[k][e] = tap[r][k + 1][e];
+                    nw[W - 2][e] = x[r].v[e];
+                }
+                store_taps<E, VEC, W>(a, (int64_t)slot[r] * a.cslot + (int64_t)c0 * a.cc, nw);
+            }
+        }
+        const OutSeg<E> out = out_seg<E>(a, b0 + r, c0);
+        store_floats<E, VEC>(out.p, acc);
+    }
+}
+
 // Every other width (1, 5..16): a thread per (row, strip, channel) that reads each tap
 // where it lies. Same ownership of the windows.
 template <typename E>
@@ -597,14 +678,14 @@ conv_prefill_any_kernel(const __grid_constant__ ConvPrefillArgs a, const int cha
 // A CTA per (row, 128 bytes of channels) of a draft tree of up to kMaxNodes nodes. W: the
 // width, or 0 for any.
 template <typename E, int W>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 7)
 conv_tree_kernel(const __grid_constant__ ConvPrefillArgs a, const int blocks, const bool vec)
 {
-    constexpr int V = Vec16<E>::kElems, kCh = 8 * V, kUnits = 8;
+    constexpr int V = Vec16<E>::kElems, kUnits = 8, kCh = kUnits * V;
     constexpr int kMaxW = W ? W : 16;
     __shared__ __align__(16) E s_in[(kMaxNodes + kMaxW - 1) * kCh];
-    __shared__ uint8_t s_row[kMaxNodes][kMaxW];         // rows of the inputs, newest first
-    __shared__ uint8_t s_bad[kMaxNodes];
+    constexpr int kRowB = W && W <= 4 ? 4 : 16;
+    __shared__ __align__(4) uint8_t s_row[kMaxNodes][kRowB];    // rows of the inputs, newest first
     __shared__ int s_par[kMaxNodes];
     const int width = W ? W : a.width, taps = width - 1;
     const int b = blockIdx.x / blocks, tid = threadIdx.x;
@@ -618,10 +699,11 @@ conv_tree_kernel(const __grid_constant__ ConvPrefillArgs a, const int blocks, co
     }
     // this thread's unit of V channels, and where its outputs go
     const int u = tid % kUnits, cu = c0 + u * V;
+    const OutSeg<E> seg = out_seg<E>(a, b, min(cu, channels - 1));
     const auto store = [&](int t, const float (&f)[V]) {
-        if (vec && cu < channels) {             // whole and inside one segment
-            const OutSeg<E> o = out_seg<E>(a, b, cu);
-            store_floats<E, V>(o.p + t * o.ld, f);
+        if (vec) {                              // whole and inside one segment
+            if (cu < channels)
+                store_floats<E, V>(seg.p + t * seg.ld, f);
         } else {
 #pragma unroll
             for (int e = 0; e < V; ++e)
@@ -711,7 +793,8 @@ conv_tree_kernel(const __grid_constant__ ConvPrefillArgs a, const int blocks, co
                 }
             }
         }
-        s_bad[tid] = bad;
+        if (bad)
+            s_row[tid][0] = kBad;               // (no row has this number)
         if (bad && c0 == 0 && a.err)
             atomicOr(a.err, SSU_FLAG_TREE);
     }
@@ -723,31 +806,34 @@ conv_tree_kernel(const __grid_constant__ ConvPrefillArgs a, const int blocks, co
 #pragma unroll
         for (int e = 0; e < V; ++e)
             acc[e] = bias[e];
-        const auto add = [&](int k, const float (&wk)[V]) {
+        const auto add = [&](int row, const float (&wk)[V]) {
             float f[V];
-            widen_chunk<E, V>(load_chunk<E, V>(s_in, s_row[t][width - 1 - k] * kCh + u * V), f);
+            widen_chunk<E, V>(load_chunk<E, V>(s_in, row * kCh + u * V), f);
             fma_vec<V>(acc, wk, f);
         };
+        const uint32_t rows = *reinterpret_cast<const uint32_t *>(s_row[t]);
+        if ((rows & 255) == kBad) {
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                acc[e] = 0.f;
+            store(t, acc);
+            continue;
+        }
         if constexpr (W > 0) {
 #pragma unroll
             for (int k = 0; k < W; ++k)
-                add(k, w[k]);
+                add(rows >> (8 * (W - 1 - k)) & 255, w[k]);
         } else {
             for (int k = 0; k < width; ++k) {
 #pragma unroll
                 for (int e = 0; e < V; ++e)
                     w[0][e] = widen<E>(
                         static_cast<const E *>(a.w)[(int64_t)min(cu + e, channels - 1) * width + k]);
-                add(k, w[0]);
+                add(s_row[t][width - 1 - k], w[0]);
             }
         }
         if (a.silu)
             silu_vec<E, V>(acc);
-        if (s_bad[t]) {
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                acc[e] = 0.f;
-        }
         store(t, acc);
     }
 }
@@ -843,12 +929,22 @@ int launch_w(const ConvPrefillArgs &a, cudaStream_t s)
         return launch_kernel(conv_prefill_any_kernel<E>, (unsigned)blocks, kThreads, 0, s, a, groups,
                              strips);
     else
-        // one token at a time keeps few registers, which is what a single token wants; rows of
-        // single channels load eight ahead
+        // few tokens want few registers: one at a time; else rows of single channels load
+        // eight ahead
         return a.T < 8 ? launch_kernel(conv_prefill_kernel<E, VEC, W, 1>, (unsigned)blocks, kThreads, 0,
                                        s, a, groups, strips)
                        : launch_kernel(conv_prefill_kernel<E, 1, W, 8>, (unsigned)blocks, kThreads,
                                        0, s, a, groups, strips);
+}
+
+template <typename E, int W> int launch_token(const ConvPrefillArgs &a, cudaStream_t s)
+{
+    constexpr int VEC = Vec16<E>::kElems / 2;
+    const int groups = (a.x_dim + 2 * a.bc_dim) / VEC;
+    const int64_t blocks = ((int64_t)groups * ((a.active + 1) / 2) + kThreads - 1) / kThreads;
+    if (blocks > 0x7fffffffLL)
+        return SSU_ERR_SHAPE;
+    return launch_kernel(conv_token_kernel<E, VEC, W>, (unsigned)blocks, kThreads, 0, s, a, groups);
 }
 
 template <typename E, int W> int launch_stream(const ConvPrefillArgs &a, cudaStream_t s)
@@ -864,7 +960,7 @@ template <typename E, int W> int launch_stream(const ConvPrefillArgs &a, cudaStr
 
 template <typename E, int W> int launch_tree(const ConvPrefillArgs &a, bool vec, cudaStream_t s)
 {
-    const int per = 8 * Vec16<E>::kElems;
+    const int per = 8 * Vec16<E>::kElems;           // channels of a CTA
     const int blocks = (a.x_dim + 2 * a.bc_dim + per - 1) / per;
     if ((int64_t)blocks * a.active > 0x7fffffffLL)
         return SSU_ERR_SHAPE;
@@ -902,6 +998,13 @@ template <typename E> int launch_e(ConvPrefillArgs a, cudaStream_t s)
         case 2: return launch_stream<E, 2>(a, s);
         case 3: return launch_stream<E, 3>(a, s);
         case 4: return launch_stream<E, 4>(a, s);
+        }
+    }
+    if (a.T == 1) {
+        switch (a.width) {
+        case 2: return launch_token<E, 2>(a, s);
+        case 3: return launch_token<E, 3>(a, s);
+        case 4: return launch_token<E, 4>(a, s);
         }
     }
     // half vectors: fewer registers a thread and twice the threads for the few tokens

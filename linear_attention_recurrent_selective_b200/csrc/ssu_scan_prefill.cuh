@@ -19,13 +19,14 @@
 // butterfly, and finishes and stores their outputs. The next group's steps are formed while
 // this one runs. Rows run longest first.
 //
-// Few rows leave most of the card idle, so a long row may be split over a cluster of CTAs,
-// each taking a segment of its tokens. The recurrence is linear in the state: a segment
-// started from zero ends in h0, and started from h in exp(A sum dt) h + h0. So every CTA
-// but the first runs its segment from zero without outputs (about 2/3 of the work), the
-// ends are exchanged through distributed shared memory, each CTA folds those before it into
-// its true start, and runs its segment again with outputs. The first CTA starts from the
-// true state and runs once; its segment is 2/3 as long, so that the CTAs meet in time.
+// Few rows leave most of the card idle, so a long row may be cut into segments of tokens for
+// the CTAs of a cluster and the warps of each. The recurrence is linear in the state: a
+// segment started from zero ends in h0, and started from h in exp(A sum dt) h + h0. So every
+// team but the first runs its segment from zero without outputs (about 2/3 of the work), the
+// ends are exchanged (through distributed shared memory between CTAs), each team folds those
+// before it into its true start, and runs its segment again with outputs. The first team
+// starts from the true state and runs once; its segment is 2/3 as long, so that the teams
+// meet in time.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -40,25 +41,28 @@ namespace cg = cooperative_groups;
 
 constexpr int kStates = 8;            // of a lane
 constexpr int kMinWarps = 16;         // of an SM: at most 128 registers a thread
-constexpr int kFill = 592;            // CTAs that give 148 SMs four each
+constexpr int kFill = 2700;           // warps of a full card (148 SMs of 18)
 constexpr int kMaxParts = 16;         // CTAs of a cluster (above 8 by opt-in)
 
-// CH: neighbouring channels of a lane, 1 or 2.
-template <int N, int CH> struct Tile {
+// CH: neighbouring channels of a lane, 1 or 2. TM: teams of a CTA, each with a segment of the
+// row's tokens; one team is the whole CTA, more are a warp each.
+template <int N, int CH, int TM> struct Tile {
     static constexpr int kL = N / kStates;                              // lanes of a channel
-    static constexpr int kWarps = N == 256 ? 8 / CH : (N >= 32 ? 4 : 4 / CH);
-    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kWarps = TM > 1 ? 1 : N == 256 ? 8 / CH : (N >= 32 ? 4 : 4 / CH);
+    static constexpr int kThreads = 32 * kWarps;                        // of a team
     // channels of a CTA: a multiple of 8, so that a row of them is whole 16-byte units
     static constexpr int kCh = kThreads / kL * CH;
-    static constexpr int kTok = N <= 64 ? 32 : (N == 128 ? 16 : 8);     // tokens of a chunk
+    static constexpr int kTok = N <= 64 && TM == 1 ? 32 : N <= 128 ? 16 : 8;   // of a chunk
     static constexpr int kOwn = kL >= 4 ? 1 : 4 / kL;                   // tokens of a lane, of 4
     // the lane's values of a group as packed pairs: of its two channels, or of two tokens
     static constexpr int kPr = CH == 2 ? kOwn : (kOwn + 1) / 2;
-    // shared memory: B and C widened, two stages of [2][kTok][N]; two stages of raw x, dt, z,
-    // B, C; where rows are split, the segment's end state [kCh][N] and sum of steps [kCh]
+    // shared memory of a team: B and C widened, two stages of [2][kTok][N]; two stages of raw
+    // x, dt, z, B, C. Behind the teams', where rows are split: the end state [kCh][N] and sum
+    // of steps [kCh] of each team's segment, and of the CTA's where it has several
     static constexpr int kWide = 2 * kTok * N * 4;
     static constexpr int kFixed = 2 * kWide;
-    static constexpr int kEnds = kCh * N * 4 + kCh * 4;
+    static constexpr int kEnd = kCh * N + kCh;                          // floats of one end
+    static constexpr int kEnds = (TM > 1 ? TM + 1 : 1) * kEnd * 4;
     static_assert(kCh % 8 == 0, "");
 };
 
@@ -69,10 +73,10 @@ struct Raw {
     int x, dt, z, B, C, bytes;
 };
 
-template <int N, int CH>
+template <int N, int CH, int TM>
 __host__ __device__ __forceinline__ Raw raw_layout(int ex, int ed, int eb, bool z)
 {
-    using T = Tile<N, CH>;
+    using T = Tile<N, CH, TM>;
     Raw r;
     r.x = 0;
     r.dt = T::kTok * T::kCh * ex;
@@ -237,15 +241,15 @@ struct Block {
 
 // Run tokens [t_begin, t_end) of the row through the lane's states; kOut: form the outputs.
 // DT: the type of x, dt, z, B and C where they share it and it was compiled in, else -1.
-template <int N, int CH, int DT, bool kOut>
+template <int N, int CH, int TM, int DT, bool kOut>
 __device__ __forceinline__ void run_tokens(const ScanArgs &a, Lane<CH> &st, uint8_t *smem, int b,
                                            const Block blk, int t_begin, int t_end)
 {
-    using T = Tile<N, CH>;
+    using T = Tile<N, CH, TM>;
     constexpr int kL = T::kL, kTok = T::kTok, kCh = T::kCh, kOwn = T::kOwn, kPr = T::kPr;
     constexpr int kP = kStates / 2, kThreads = T::kThreads;
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int ln = lane % kL, n0 = ln * kStates, ch = tid / kL * CH;
+    const int tid = TM > 1 ? threadIdx.x % kThreads : threadIdx.x;      // in the team
+    const int ln = tid % kL, n0 = ln * kStates, ch = tid / kL * CH;
     const int64_t row = (int64_t)b * a.T;
 
     // rows of this CTA's channels, from token 0 of the row
@@ -253,7 +257,7 @@ __device__ __forceinline__ void run_tokens(const ScanArgs &a, Lane<CH> &st, uint
     const int bct = DT < 0 ? a.bc_dtype : DT;
     const int ex = esize(xt), ed = esize(dtt), eb = esize(bct);
     const bool gated = kOut && a.z, softplus = a.softplus;
-    const Raw lay = raw_layout<N, CH>(ex, ed, eb, a.z);
+    const Raw lay = raw_layout<N, CH, TM>(ex, ed, eb, a.z);
     uint8_t *const raw0 = smem + T::kFixed;
     const char *const gx = static_cast<const char *>(a.x) + (row * a.ldx + blk.d0) * ex;
     const char *const gd = static_cast<const char *>(a.dt) + (row * a.lddt + blk.d0) * ed;
@@ -292,7 +296,10 @@ __device__ __forceinline__ void run_tokens(const ScanArgs &a, Lane<CH> &st, uint
             widen_rows<kThreads, kTok * N>(s_B, r + lay.B, bct, a.vec & 16, tid);
             if (kOut)
                 widen_rows<kThreads, kTok * N>(s_C, r + lay.C, bct, a.vec & 32, tid);
-            __syncthreads();            // the chunk is here, the other stage is free
+            if (TM > 1)
+                __syncwarp();           // the chunk is here, the other stage is free
+            else
+                __syncthreads();
         }
         if (const int t1 = t0 + kTok; t1 < t_end) {
             uint8_t *const to = raw0 + (stage ^ 1) * lay.bytes;
@@ -404,16 +411,19 @@ __device__ __forceinline__ void run_tokens(const ScanArgs &a, Lane<CH> &st, uint
     }
 }
 
-template <int N, int CH, int DT>
-__global__ void __launch_bounds__(Tile<N, CH>::kThreads, kMinWarps / Tile<N, CH>::kWarps)
+template <int N, int CH, int TM, int DT>
+__global__ void __launch_bounds__(Tile<N, CH, TM>::kThreads * TM,
+                                  kMinWarps / (Tile<N, CH, TM>::kWarps * TM))
 scan_prefill_kernel(const __grid_constant__ ScanArgs a, const int blocks, const int parts)
 {
-    using T = Tile<N, CH>;
+    using T = Tile<N, CH, TM>;
     constexpr int S = kStates, kP = S / 2, kL = T::kL, kCh = T::kCh, kThreads = T::kThreads;
+    constexpr int kEnd = T::kEnd;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int s_len[kRankMax], s_row;
 
-    const int tid = threadIdx.x;
+    const int team = TM > 1 ? threadIdx.x / kThreads : 0;
+    const int tid = TM > 1 ? threadIdx.x % kThreads : threadIdx.x;      // in the team
     const int part = blockIdx.x % parts, unit = blockIdx.x / parts;
     const int b = ranked_row(a, unit / blocks, s_len, &s_row);
     const int per = a.D / a.G, of_group = blocks / a.G;     // channels, blocks of a group
@@ -422,7 +432,7 @@ scan_prefill_kernel(const __grid_constant__ ScanArgs a, const int blocks, const 
     blk.d0 = blk.g * per + unit % blocks % of_group * kCh;
     blk.n = min(kCh, (blk.g + 1) * per - blk.d0);
     const int slot = a.idx ? a.idx[b] : b;
-    const bool first = unit % blocks == 0 && part == 0 && tid == 0;
+    const bool first = unit % blocks == 0 && part == 0 && threadIdx.x == 0;
     if (slot >= a.P) {                                      // caller bug: skip and report
         if (first && a.err)
             atomicOr(a.err, SSU_FLAG_INDEX_RANGE);
@@ -430,7 +440,7 @@ scan_prefill_kernel(const __grid_constant__ ScanArgs a, const int blocks, const 
     }
     if (slot < 0) {                                         // padding row: zeros
         if (a.out && part == 0) {
-            for (int64_t v = tid; v < (int64_t)a.T * kCh; v += kThreads)
+            for (int64_t v = threadIdx.x; v < (int64_t)a.T * kCh; v += kThreads * TM)
                 if (v % kCh < blk.n)
                     st_f32(a.out, a.x_dtype, ((int64_t)b * a.T + v / kCh) * a.D + blk.d0 + v % kCh,
                            0.f);
@@ -451,12 +461,14 @@ scan_prefill_kernel(const __grid_constant__ ScanArgs a, const int blocks, const 
     const int ln = tid % kL, n0 = ln * S, ch = tid / kL * CH;
     const int64_t pool0 = (int64_t)slot * a.slot_stride;
     Lane<CH> s;
+    const int seg = part * TM + team, segs = parts * TM;    // this team's segment, of so many
+    const bool last = seg + 1 == segs;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         const int64_t at = ((int64_t)blk.d0 + min(ch + c, blk.n - 1)) * N + n0;
         float h[S] = {}, rate[S];
         load_decay_rates<S>(a.A, at, rate);
-        if (part == 0)
+        if (seg == 0)
             load_states<S>(a.state, a.state_dtype, pool0 + at, h);
 #pragma unroll
         for (int i = 0; i < kP; ++i) {
@@ -466,60 +478,86 @@ scan_prefill_kernel(const __grid_constant__ ScanArgs a, const int blocks, const 
         s.sum[c] = 0.f;
     }
 
-    // this CTA's tokens: segments in units of a chunk, the first 2 shares, the others 3
+    // segments in units of a chunk: the first 2 shares, the others 3
     cg::cluster_group cluster = cg::this_cluster();
-    const int chunks = (L + T::kTok - 1) / T::kTok, shares = 3 * parts - 1;
+    const int chunks = (L + T::kTok - 1) / T::kTok, shares = 3 * segs - 1;
     const auto bound = [&](int p) {
         return p == 0 ? 0 : min((int)((int64_t)chunks * (3 * p - 1) / shares) * T::kTok, L);
     };
-    const int t0 = bound(part), t1 = part + 1 == parts ? L : bound(part + 1);
-    const bool last = part + 1 == parts;
-    const Raw lay = raw_layout<N, CH>(esize(a.x_dtype), esize(a.dt_dtype), esize(a.bc_dtype), a.z);
-    float *const s_end = reinterpret_cast<float *>(smem + T::kFixed + 2 * lay.bytes);
-    float *const s_sum = s_end + kCh * N;
+    const int t0 = bound(seg), t1 = last ? L : bound(seg + 1);
+    const Raw lay =
+        raw_layout<N, CH, TM>(esize(a.x_dtype), esize(a.dt_dtype), esize(a.bc_dtype), a.z);
+    const int team_bytes = T::kFixed + 2 * lay.bytes;
+    float *const ends = reinterpret_cast<float *>(smem + TM * team_bytes);  // [TM (+ 1)][kEnd]
+    const int end_at = ch * N + n0, sum_at = kCh * N + ch;                  // this lane's, in one
+    float *const cta_end = TM > 1 ? ends + TM * kEnd : ends;
+    const auto put_end = [&](float *end) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+#pragma unroll
+            for (int i = 0; i < kP; ++i)
+                *reinterpret_cast<float2 *>(end + end_at + c * N + 2 * i) = s.h[c][i];
+            if (ln == 0)
+                end[sum_at + c] = s.sum[c];
+        }
+    };
+    // the state behind a segment that ends in `end`: `first` replaces it, others let it decay
+    // over their steps and add what they end in from zero
+    const auto fold = [&](const float *end, bool replace) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const float sum = end[sum_at + c];
+#pragma unroll
+            for (int i = 0; i < kP; ++i) {
+                const float2 e = *reinterpret_cast<const float2 *>(end + end_at + c * N + 2 * i);
+                const float2 f = make_float2(exp2_fast(sum * s.rate[c][i].x),
+                                             exp2_fast(sum * s.rate[c][i].y));
+                s.h[c][i] = replace ? e : fma2(s.h[c][i], f, e);
+            }
+            s.sum[c] += sum;
+        }
+    };
 #pragma unroll 1
-    for (int pass = part > 0 && last ? 1 : 0; pass < (part ? 2 : 1); ++pass) {
+    for (int pass = 0; pass < 2; ++pass) {
         if (pass == 1) {
-            // every end is there: fold those before this segment into its start
-            cluster.sync();
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                for (int q = 0; q < part; ++q) {
-                    const float *const end = cluster.map_shared_rank(s_end, q) + (ch + c) * N + n0;
-                    const float sum = q ? *cluster.map_shared_rank(s_sum + ch + c, q) : 0.f;
-#pragma unroll
-                    for (int i = 0; i < kP; ++i) {
-                        const float2 e = *reinterpret_cast<const float2 *>(end + 2 * i);
-                        const float2 f = make_float2(exp2_fast(sum * s.rate[c][i].x),
-                                                     exp2_fast(sum * s.rate[c][i].y));
-                        s.h[c][i] = q ? fma2(s.h[c][i], f, e) : e;
-                    }
+            if (segs == 1)
+                break;
+            put_end(ends + team * kEnd);
+            if (TM > 1) {
+                __syncthreads();
+                if (team == 0 && part + 1 < parts) {        // the whole CTA's end
+                    const Lane<CH> mine = s;
+                    for (int q = 1; q < TM; ++q)
+                        fold(ends + q * kEnd, false);
+                    put_end(cta_end);
+                    s = mine;
                 }
             }
-            cluster.barrier_arrive();           // the others' ends are read
-        }
-        if (a.out && (pass == 1 || part == 0))
-            run_tokens<N, CH, DT, true>(a, s, smem, b, blk, t0, t1);
-        else if (pass == 0 || last)
-            run_tokens<N, CH, DT, false>(a, s, smem, b, blk, t0, t1);
-        if (pass == 0 && parts > 1) {
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-#pragma unroll
-                for (int i = 0; i < kP; ++i)
-                    *reinterpret_cast<float2 *>(s_end + (ch + c) * N + n0 + 2 * i) = s.h[c][i];
-                if (ln == 0)
-                    s_sum[ch + c] = s.sum[c];
+            if (parts > 1)
+                cluster.sync();
+            // every end is there: fold those before this segment into its start
+            if (seg > 0) {
+#pragma unroll 4
+                for (int q = 0; q < part; ++q)
+                    fold(cluster.map_shared_rank(cta_end, q), q == 0);
+                for (int q = 0; q < team; ++q)
+                    fold(ends + q * kEnd, part == 0 && q == 0);
             }
+            if (parts > 1)
+                cluster.barrier_arrive();                   // the others' ends are read
+            if (seg == 0)
+                break;
         }
+        // the first segment starts from the true state and runs once, with outputs; of the
+        // others the last needs no end, and all run with outputs in the second pass
+        uint8_t *const own_smem = smem + team * team_bytes;
+        if (a.out && (pass == 1 || seg == 0))
+            run_tokens<N, CH, TM, DT, true>(a, s, own_smem, b, blk, t0, t1);
+        else if (pass == 0 ? !last || segs == 1 : last)
+            run_tokens<N, CH, TM, DT, false>(a, s, own_smem, b, blk, t0, t1);
     }
-    if (parts > 1) {
-        if (part == 0) {
-            cluster.sync();
-            cluster.barrier_arrive();
-        }
+    if (parts > 1)
         cluster.barrier_wait();                 // no CTA leaves while its end may be read
-    }
 
     if (a.update && last) {
 #pragma unroll
@@ -537,15 +575,16 @@ scan_prefill_kernel(const __grid_constant__ ScanArgs a, const int blocks, const 
     }
 }
 
-// Rows are split into p parts while the CTAs fill less than half of the card's room for them
-// and every part keeps at least 64 tokens: that costs (3 p + 2) / (3 p - 1) of a row's work
-// and runs it p times as wide, so two parts gain nothing.
-int parts_of(int64_t units, int T)
+// How many segments a row is cut into: while that leaves at most kFill warps and every
+// segment 64 tokens. s segments cost (5 s - 2) / (3 s - 1) of a row's work (1.6 for 4 and
+// more) but run s times as wide, in 6 / (3 s - 1) of its steps, so fewer than four gain
+// nothing. `warps`: of the call with one segment a row; `most`: that the form can take.
+int segments_of(int64_t warps, int T, int most)
 {
-    int p = 1;
-    while (p < kMaxParts && units * p * 2 <= kFill && T >= 128 * p)
-        p *= 2;
-    return p < 4 ? 1 : p;
+    int s = 1;
+    while (s < most && warps * s * 2 <= kFill && T >= 128 * s)
+        s *= 2;
+    return s < 4 ? 1 : s;
 }
 
 // Clusters of more than 8 CTAs need the kernel's consent, given once per device.
@@ -563,28 +602,30 @@ template <auto kernel> bool wide_clusters()
     return ok[dev];
 }
 
-template <int N, int CH> int64_t blocks_of(const ScanArgs &a)
+template <int N, int CH, int TM> int64_t blocks_of(const ScanArgs &a)
 {
-    constexpr int kCh = Tile<N, CH>::kCh;
+    constexpr int kCh = Tile<N, CH, TM>::kCh;
     return (int64_t)a.G * ((a.D / a.G + kCh - 1) / kCh);
 }
 
-template <int N, int CH, int DT> int launch_c(const ScanArgs &a, cudaStream_t s)
+// `segs` segments a row, a multiple of TM.
+template <int N, int CH, int TM, int DT>
+int launch_c(const ScanArgs &a, int segs, cudaStream_t s)
 {
-    using T = Tile<N, CH>;
-    const int64_t blocks = blocks_of<N, CH>(a), units = blocks * a.active;
-    const int parts = parts_of(units, a.T);
+    using T = Tile<N, CH, TM>;
+    const int64_t blocks = blocks_of<N, CH, TM>(a), units = blocks * a.active;
+    const int parts = segs / TM;
     const int64_t grid = units * parts;
     if (blocks > 0x7fffffffLL || grid > 0x7fffffffLL)
         return SSU_ERR_SHAPE;
-    const Raw lay = raw_layout<N, CH>(esize(a.x_dtype), esize(a.dt_dtype), esize(a.bc_dtype), a.z);
+    const Raw lay = raw_layout<N, CH, TM>(esize(a.x_dtype), esize(a.dt_dtype), esize(a.bc_dtype), a.z);
     // the largest layout (fp32 inputs) sets the kernel's shared-memory limit
     constexpr int kMost =
-        T::kFixed + 2 * (T::kTok * T::kCh * 12 + T::kTok * N * 8) + T::kEnds;
-    const KernelFacts *f = kernel_facts<scan_prefill_kernel<N, CH, DT>>(T::kThreads, kMost);
+        TM * (T::kFixed + 2 * (T::kTok * T::kCh * 12 + T::kTok * N * 8)) + T::kEnds;
+    const KernelFacts *f = kernel_facts<scan_prefill_kernel<N, CH, TM, DT>>(T::kThreads * TM, kMost);
     if (!f || f->status != SSU_OK)
         return SSU_ERR_CUDA;
-    if (parts > 8 && !wide_clusters<scan_prefill_kernel<N, CH, DT>>())
+    if (parts > 8 && !wide_clusters<scan_prefill_kernel<N, CH, TM, DT>>())
         return SSU_ERR_CUDA;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -593,12 +634,12 @@ template <int N, int CH, int DT> int launch_c(const ScanArgs &a, cudaStream_t s)
     attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(T::kThreads);
-    cfg.dynamicSmemBytes = T::kFixed + 2 * lay.bytes + (parts > 1 ? T::kEnds : 0);
+    cfg.blockDim = dim3(T::kThreads * TM);
+    cfg.dynamicSmemBytes = TM * (T::kFixed + 2 * lay.bytes) + (segs > 1 ? T::kEnds : 0);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = parts > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, scan_prefill_kernel<N, CH, DT>, a, (int)blocks, parts) ==
+    return cudaLaunchKernelEx(&cfg, scan_prefill_kernel<N, CH, TM, DT>, a, (int)blocks, parts) ==
                    cudaSuccess
                ? SSU_OK
                : SSU_ERR_CUDA;
@@ -606,15 +647,27 @@ template <int N, int CH, int DT> int launch_c(const ScanArgs &a, cudaStream_t s)
 
 // Two channels a lane halve the exchanges between lanes and the reads of B and C, at twice
 // the registers: better from 64 states on (8 lanes a channel), where that leaves every SM
-// eight warps; one channel a lane is better below.
+// eight warps; one channel a lane is better below. Segments go to the CTAs of a cluster, and
+// up to 32 states (where a warp's channels still make whole 16-byte units of a row) to the
+// four warps of each.
 template <int N, int DT> int launch_n(const ScanArgs &a, cudaStream_t s)
 {
+    const int64_t one = blocks_of<N, 1, 1>(a) * Tile<N, 1, 1>::kWarps;
+    if (one > 0x7fffffffLL)
+        return SSU_ERR_SHAPE;
     if constexpr (N >= 64) {
-        const int64_t warps = blocks_of<N, 2>(a) * Tile<N, 2>::kWarps * a.active;
-        if (warps >= 1184)
-            return launch_c<N, 2, DT>(a, s);
+        const int64_t two = blocks_of<N, 2, 1>(a) * Tile<N, 2, 1>::kWarps;
+        if (two * a.active >= kFill / 2)
+            return launch_c<N, 2, 1, DT>(a, 1, s);
     }
-    return launch_c<N, 1, DT>(a, s);
+    const int64_t warps = one * a.active;
+    if constexpr (N <= 32) {
+        const int segs = segments_of(warps, a.T, 4 * kMaxParts);
+        if (segs > 1)
+            return launch_c<N, 1, 4, DT>(a, segs, s);
+        return launch_c<N, 1, 1, DT>(a, 1, s);
+    }
+    return launch_c<N, 1, 1, DT>(a, segments_of(warps, a.T, kMaxParts), s);
 }
 
 template <int DT> int launch_dt(const ScanArgs &a, cudaStream_t s)

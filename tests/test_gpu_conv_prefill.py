@@ -253,3 +253,17 @@ def test_refusals():
         ssu.ssu_conv_prefill(rows, w, pool, x, B, C, **{**kw, "conv_strides": (96, 2, 1)})
     with pytest.raises(ValueError):
         ssu.ssu_conv_replay(rows, pool, torch.zeros(3, dtype=torch.int32, device="cuda"), **kw)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("width", [2, 3, 4, 5])
+@pytest.mark.parametrize("layout", ["channel", "tap", "spread"])
+def test_single_tokens(dtype, width, layout):
+    """One token a row, an odd number of rows, with padding, an index past the pool and lengths
+    of zero and beyond one."""
+    c = make(width, 9, 1, 64, 16, width, dtype, layout, pad=8,
+             slots=[3, -1, 99, 0, 5, 1, 11, 7, 2])
+    lengths = torch.tensor([1, 1, 1, 0, 3, -2, 1, 1, 1], dtype=torch.int32)
+    check(c, lengths)
+    check(c, active=6)
+    check(c, update=False, silu=False)

@@ -160,6 +160,16 @@ def test_long_rows_of_few_channels(T, N):
     assert same_bits(again, o) and same_bits(same, pool)
 
 
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+@pytest.mark.parametrize("ch,G,xdt", [(1, 1, F32), (70, 2, BF16), (33, 3, F16)])
+def test_one_long_row(N, ch, G, xdt):
+    """One row cut into as many segments as there are."""
+    c = make(N + ch, 1, 4500, ch, G, N, xdt, F32 if N == 8 else None)
+    c["A"] = c["A"] * 0.05
+    check(c)
+    check(c, torch.tensor([4097], dtype=torch.int32), out=False)
+
+
 def test_options_padding_and_flags():
     c = make(2, 6, 9, 24, 1, 32, F32, slots=[3, -1, 99, 0, 5, 1], z=False, D=False, bias=False,
              positive=True)
