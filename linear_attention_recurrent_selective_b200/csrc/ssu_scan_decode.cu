@@ -141,8 +141,7 @@ scan_decode_kernel(const __grid_constant__ ScanArgs a, const int blocks)
         if (live[r]) {
 #pragma unroll
             for (int i = 0; i < kP; ++i) {
-                const float2 v = mul2(d2, make_float2(rate[2 * i], rate[2 * i + 1]));
-                const float2 e = make_float2(exp2_fast(v.x), exp2_fast(v.y));
+                const float2 e = decay2(d2, make_float2(rate[2 * i], rate[2 * i + 1]));
                 const float2 s = fma2(make_float2(h[r][2 * i], h[r][2 * i + 1]), e,
                                       mul2(x2, pair_of<kS>(rB[r], bct, i)));
                 acc = fma2(s, pair_of<kS>(rC[r], bct, i), acc);

@@ -364,8 +364,7 @@ __device__ __forceinline__ void run_tokens(const ScanArgs &a, Lane<CH> &st, uint
                     float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int i = 0; i < kP; ++i) {
-                        const float2 v = mul2(d2, st.rate[c][i]);
-                        const float2 e = make_float2(exp2_fast(v.x), exp2_fast(v.y));
+                        const float2 e = decay2(d2, st.rate[c][i]);
                         st.h[c][i] = fma2(st.h[c][i], e, mul2(x2, Bv[i]));
                         if (kOut)
                             acc = i ? fma2(st.h[c][i], Cv[i], acc) : mul2(st.h[c][i], Cv[i]);
@@ -383,9 +382,9 @@ __device__ __forceinline__ void run_tokens(const ScanArgs &a, Lane<CH> &st, uint
                 for (int p = 0; p < kPr; ++p) {
                     const int ta = t + first_of(p), tb = t + second_of(p);
                     o[p] = fma2(skip, x[p], o[p]);
-                    // (without a gate this reads other inputs and drops the product)
-                    const float2 z = elems_at<CH == 2>(r + lay.z, xt, ta * kCh + ch,
-                                                       tb * kCh + ch + CH - 1);
+                    // (without a gate this reads x, a tile of the same size, and drops the product)
+                    const float2 z = elems_at<CH == 2>(r + (gated ? lay.z : lay.x), xt,
+                                                       ta * kCh + ch, tb * kCh + ch + CH - 1);
                     const float2 go = mul2(o[p], gate2(z, xt));
                     o[p].x = gated ? go.x : o[p].x;
                     o[p].y = gated ? go.y : o[p].y;

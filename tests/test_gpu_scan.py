@@ -303,3 +303,30 @@ def test_refusals():
     with pytest.raises(ValueError):
         ssu.scan_prefill(*good, P=c["P"], context_lengths=torch.zeros(3, dtype=torch.int32,
                                                                        device="cuda"))
+
+
+@pytest.mark.parametrize("N", [8, 16, 128])
+def test_steps_of_zero_keep_every_bit(N):
+    c = make(12, 2, 70, 24, 1, N, F32, z=False, bias=False)
+    c["dt"][0].zero_()
+    _, pool, _ = run(c, softplus=False)
+    assert same_bits(pool, c["pool"])
+    step = c["pool"].cuda()
+    for _ in range(3):
+        run_decode(c, 0, step, softplus=False)
+    assert same_bits(step, c["pool"])
+
+
+def test_errors_do_not_gather():
+    """500 slow steps: the states' error stays that of a few roundings (a decay that is half a
+    step low every time would be off by 500 * 2^-25 = 1.5e-5)."""
+    c = make(13, 2, 500, 32, 1, 16, F32, z=False, bias=False)
+    c["dt"] = (torch.full_like(c["dt"][0], 0.05) * (1 + 0.1 * c["x"][0].cos()), c["dt"][1])
+    c["A"] = -0.02 * torch.rand(32, 16, generator=po.generator(3))
+    _, pool, _ = run(c, softplus=False)
+    _, state, _, _, _ = plain(c, softplus=False)
+    live = c["slots"].long()
+    got = pool.view(c["P"], 32, 16).double()[live]
+    # 500 independent roundings of a half step each, four deep, add up to about
+    # sqrt(500) * 4 * 2^-25 = 2.7e-6 of the state's size
+    assert ((got - state[live]).norm() / state[live].norm()).item() < 2.7e-6
