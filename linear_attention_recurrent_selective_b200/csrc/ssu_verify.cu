@@ -52,6 +52,7 @@ __device__ __forceinline__ float mass_of(float v)
 struct Shared {
     int parent[kMaxTree], token[kMaxTree], first_child[kMaxTree], path[kMaxTree];
     double child_mass[kMaxTree];
+    float u[kMaxTree];
     int drop[kMaxTree];               // tokens without mass in the row to draw from
     int ndrop, stop, root, n, end;
     double warp_sum[kWarps];
@@ -446,6 +447,7 @@ verify_kernel(const __grid_constant__ VerifyArgs a)
         if (tid < L) {
             up = par[tid];
             x = tokens[tid];
+            s.u[tid] = u[tid];
             const bool child = up >= 0 && up < L;
             if (up == -1)
                 atomicMin(&s.root, tid);
@@ -475,7 +477,7 @@ verify_kernel(const __grid_constant__ VerifyArgs a)
             for (int j = 0; j <= tid; ++j)
                 if (s.parent[j] == up)
                     run += s.child_mass[j];
-            if ((double)u[up] < run)
+            if ((double)s.u[up] < run)
                 atomicMin(&s.first_child[up], tid);
         }
         __syncthreads();
