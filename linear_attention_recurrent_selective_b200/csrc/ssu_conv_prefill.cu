@@ -32,7 +32,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kMaxNodes = 128;        // nodes of a draft tree
 constexpr int kBad = 255;             // in a node's list of rows: it is malformed
-constexpr int kStages = 3, kGroup = 4;  // of a thread's ring
+constexpr int kStages = 2, kGroup = 8;  // of a thread's ring
 constexpr int kStrip = 32;            // tokens of a strip, >= the widest window (16) - 1
 
 template <typename E, int VEC> struct alignas(sizeof(E) * VEC) Chunk {
@@ -431,9 +431,9 @@ conv_prefill_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups,
 // strip through a ring of its own in shared memory by cp.async, kStages groups of kGroup
 // tokens ahead, so that what is in flight does not take registers (a register prefetch of
 // one group kept 14 KB an SM in flight: 60 us for 16 rows of 512 tokens of 5376 channels in
-// bfloat16, against 43 us this way). Only its own copies are waited for: no barrier.
+// bfloat16, against 39 us this way, DRAM 38 % busy). Only its own copies are waited for: no barrier.
 template <typename E, int W>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 conv_stream_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups, const int strips)
 {
     constexpr int VEC = Vec16<E>::kElems;
@@ -512,33 +512,39 @@ conv_stream_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups, 
             widen_chunk<E, VEC>(load_chunk<E, VEC>(in, (t0 - (W - 1) + j) * a.ldx), win[j]);
     }
 
-    int stage = 0;
-    for (int t = t0; t < t1; t += kGroup) {
+    const auto token = [&](const Chunk<E, VEC> &raw, int t) {
+        float f[VEC], acc[VEC];
+        widen_chunk<E, VEC>(raw, f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            acc[e] = bias[e];
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k)
+            fma_vec<VEC>(acc, w[k], win[k]);
+        fma_vec<VEC>(acc, w[W - 1], f);
+        if (a.silu)
+            silu_vec<E, VEC>(acc);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+            for (int k = 0; k + 1 < W - 1; ++k)
+                win[k][e] = win[k + 1][e];
+            win[W - 2][e] = f[e];
+        }
+        store_floats<E, VEC>(out.p + t * out.ld, acc);
+    };
+    int stage = 0, t = t0;
+    for (; t < t1; t += kGroup) {
         fetch(t + (kStages - 1) * kGroup, stage == 0 ? kStages - 1 : stage - 1);
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        if (t + kGroup <= t1) {                 // (whole groups: the window moves by renaming)
 #pragma unroll
-        for (int u = 0; u < kGroup; ++u) {
-            if (t + u < t1) {
-                float f[VEC], acc[VEC];
-                widen_chunk<E, VEC>(ring[stage * kGroup + u][threadIdx.x], f);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    acc[e] = bias[e];
-#pragma unroll
-                for (int k = 0; k < W - 1; ++k)
-                    fma_vec<VEC>(acc, w[k], win[k]);
-                fma_vec<VEC>(acc, w[W - 1], f);
-                if (a.silu)
-                    silu_vec<E, VEC>(acc);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-#pragma unroll
-                    for (int k = 0; k + 1 < W - 1; ++k)
-                        win[k][e] = win[k + 1][e];
-                    win[W - 2][e] = f[e];
-                }
-                store_floats<E, VEC>(out.p + (t + u) * out.ld, acc);
-            }
+            for (int u = 0; u < kGroup; ++u)
+                token(ring[stage * kGroup + u][threadIdx.x], t + u);
+        } else {
+#pragma unroll 1
+            for (int u = 0; t + u < t1; ++u)
+                token(ring[stage * kGroup + u][threadIdx.x], t + u);
         }
         stage = stage + 1 == kStages ? 0 : stage + 1;
     }
