@@ -314,8 +314,8 @@ int ssu_conv_replay(const void *xbc, int x_dtype, int64_t xbc_stride, void *conv
  *   x_stride, dt_stride, z_stride, B_stride, C_stride: elements between consecutive tokens
  *            (and rows) of each, so that slices of wider rows are taken in place
  *   state    pool [P, channels, dstate] state_dtype, slot stride slot_stride elements
- *   out      [batch, T, channels] x_dtype dense; t >= L_b is not written; NULL advances the
- *            state only (C, D and z are then not read)
+ *   out      [batch, T, channels] x_dtype dense, overlapping no input; t >= L_b is not
+ *            written; NULL advances the state only (C, D and z are then not read)
  *   update_state != 0: the state after L_b tokens is stored once (not when L_b == 0);
  *            0: the pool is only read (needs out)
  * A speculative draft is verified with update_state = 0 and committed by a second call with

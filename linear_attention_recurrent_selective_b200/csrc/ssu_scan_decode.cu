@@ -7,6 +7,11 @@
 // Bound: memory. The state is read and written once (2 D N elements a row) for one
 // exponential and four multiply-adds per state; x, dt, z and out are 1/N of it each.
 //
+// Measured (B200, 256 rows of 5120 channels, 16 states, fp32 pool, bfloat16 inputs): 33.5 us,
+// 0.82 of the copy rate; issue slots are 79 % busy, the conversions of B and C and the
+// exchange between lanes ahead of the recurrence itself. Loading each operand where it is
+// used, element by element, took 71 us.
+//
 // Layout: a lane holds 4 states of a channel (one 16- or 8-byte access; 8 at N = 256), kL
 // lanes a channel, and takes four batch rows of that channel at a time: A's row (as large as
 // a row's fp32 state, but shared by the batch) is read once, and every load of the four rows

@@ -9,6 +9,14 @@
 // Bound: the special-function unit (16 exponentials a clock and SM, so one clock per
 // (token, channel) and SM at N = 16), ahead of memory (x, dt, z, out: 8 bytes).
 //
+// Measured (B200, bfloat16, 5120 channels, 16 states): 16 full rows of 512 tokens 265 us, 16
+// ragged ones 148 us, against 97 us (full: 192) for the special-function operations alone
+// (16 decays, 3 for the softplus, 2 for the gate); that unit is 73 % busy and issue slots 65 %.
+// Without the decays' exponentials the full rows take 253 of then 286 us, without softplus
+// and gate 233, without the exchanges between lanes 251, and B and C cost nothing: what
+// bounds it is the sum of what a warp issues. One row of 4099 tokens of 1000 channels: 80 us
+// in 32 segments (770 us in one).
+//
 // Layout: a lane holds 8 states of a channel, kL = N / 8 lanes a channel; a CTA takes a block
 // of neighbouring channels of one row and walks its tokens in chunks of kTok, whose raw
 // inputs arrive in shared memory by cp.async one chunk ahead (plain loads where rows are not

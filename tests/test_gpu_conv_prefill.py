@@ -68,7 +68,7 @@ LEN = [0, 1, 2, 3, 5, 32, 33, 70]
 
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
-@pytest.mark.parametrize("width", [1, 2, 3, 4, 5, 16])
+@pytest.mark.parametrize("width", [1, 2, 3, 4, 5, 7, 8, 16])
 @pytest.mark.parametrize("layout", ["channel", "tap", "spread"])
 def test_prompts_of_every_length(dtype, width, layout):
     c = make(width, 8, 70, 24, 8, width, dtype, layout, pad=8)
