@@ -250,7 +250,8 @@ __device__ __forceinline__ void store_taps(const ConvPrefillArgs &a, int64_t at,
 template <typename E, int VEC, int W>
 __device__ __forceinline__ void load_weights(const ConvPrefillArgs &a, int c0, float (&w)[W][VEC])
 {
-    constexpr int kAll = VEC * W, kC = access(kAll * sizeof(E)) / sizeof(E);
+    // (single channels are the form for unaligned rows, the weights' among them)
+    constexpr int kAll = VEC * W, kC = VEC == 1 ? 1 : access(kAll * sizeof(E)) / sizeof(E);
     Chunk<E, kC> raw[kAll / kC];
 #pragma unroll
     for (int j = 0; j < kAll / kC; ++j)

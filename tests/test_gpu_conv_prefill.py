@@ -267,3 +267,62 @@ def test_single_tokens(dtype, width, layout):
     check(c, lengths)
     check(c, active=6)
     check(c, update=False, silu=False)
+
+
+@pytest.mark.parametrize("T", [1, 5, 40])
+@pytest.mark.parametrize("width", [2, 4, 8, 16])
+def test_weights_bias_and_outputs_off_16_bytes(T, width):
+    """Contiguous tensors that start two bytes behind an aligned address."""
+    c = make(T + width, 3, T, 16, 8, width, BF16)
+
+    def off(t):
+        wide = torch.zeros(t.numel() + 1, dtype=t.dtype, device="cuda")
+        wide[1:] = t.reshape(-1).cuda()
+        return wide[1:].view(t.shape)
+    want, after, lim, _ = po.conv(c["rows"], c["weight"], c["bias"], c["pool"], c["strides"],
+                                  width, c["slots"], c["P"])
+    lim = lim + (want.abs() + lim) * po.half_step(BF16) + po.tiny(BF16)
+    for moved in ("rows", "weight", "bias", "pool", "outs"):
+        t = {k: off(c[k]) if k == moved else c[k].cuda() for k in ("rows", "weight", "bias", "pool")}
+        outs = [torch.zeros(3, T, n, dtype=BF16) for n in (16, 8, 8)]
+        outs = [off(o) if moved == "outs" else o.cuda() for o in outs]
+        ssu.ssu_conv_prefill(t["rows"], t["weight"], t["pool"], *outs, width=width,
+                             conv_strides=c["strides"], conv_bias=t["bias"],
+                             state_indices=c["slots"].cuda(), P=c["P"])
+        torch.cuda.synchronize()
+        got = torch.cat([o.cpu() for o in outs], 2).double()
+        assert ((got - want).abs() <= lim).all(), moved
+        assert same_bits(t["pool"], after), moved
+
+
+def test_nan_behind_the_rows_is_never_read():
+    c = make(3, 4, 70, 16, 8, 4, F32)
+    lengths = torch.tensor([0, 1, 33, 69], dtype=torch.int32)
+    y, pool = check(c, lengths)
+    for b, n in enumerate(lengths.tolist()):
+        c["rows"][b, n:] = NAN
+    y2, pool2 = check(c, lengths)
+    assert same_bits(y, y2) and same_bits(pool, pool2)
+
+
+def test_pool_past_32_bits():
+    """A slot whose taps lie beyond 2^31 elements of the pool."""
+    ch, W, P = 5376, 4, 140000
+    pool = torch.zeros(P, ch, W - 1, dtype=BF16, device="cuda")
+    assert (P - 1) * ch * (W - 1) > 2 ** 31
+    g = po.generator(2)
+    xbc, w = po.rand(g, 2, 3, ch).to(BF16).cuda(), po.rand(g, ch, W).to(BF16).cuda()
+    taps = po.rand(g, ch, W - 1).to(BF16)
+    pool[P - 1] = taps.cuda()
+    x = torch.empty(2, 3, ch, dtype=BF16, device="cuda")
+    slots = torch.tensor([P - 1, 5], dtype=torch.int32, device="cuda")
+    kw = dict(width=W, conv_strides=(ch * (W - 1), W - 1, 1), state_indices=slots)
+    ssu.ssu_conv_prefill(xbc, w, pool, x, **kw)
+    torch.cuda.synchronize()
+    first = (torch.cat([taps.cuda(), xbc[0, :1].T], 1).double() * w.double()).sum(1)
+    want = first * torch.sigmoid(first)
+    assert torch.allclose(x[0, 0].double(), want, rtol=2.0 ** -8, atol=1e-5)
+    assert torch.equal(pool[P - 1], xbc[0].T) and torch.equal(pool[5], xbc[1].T)
+    ssu.ssu_conv_replay(xbc, pool, torch.tensor([1, 0], dtype=torch.int32, device="cuda"), **kw)
+    assert torch.equal(pool[P - 1], torch.cat([xbc[0, 1:], xbc[0, :1]]).T)
+    assert int((pool != 0).flatten(1).any(1).sum()) == 2

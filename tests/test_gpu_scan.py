@@ -330,3 +330,72 @@ def test_errors_do_not_gather():
     # 500 independent roundings of a half step each, four deep, add up to about
     # sqrt(500) * 4 * 2^-25 = 2.7e-6 of the state's size
     assert ((got - state[live]).norm() / state[live].norm()).item() < 2.7e-6
+
+
+@pytest.mark.parametrize("T", [9, 1100])
+def test_nan_behind_the_rows_is_never_read(T):
+    c = make(14, 4, T, 24, 1, 16, F32, slots=[3, 1, -1, 0])
+    lengths = torch.tensor([0, T - 1, 3, 5], dtype=torch.int32)
+    o, pool = check(c, lengths)
+    for b, n in enumerate(lengths.tolist()):
+        for k in ("x", "dt", "B", "C", "z"):
+            c[k][0][b, 0 if b == 2 else n:] = NAN
+    o2, pool2 = check(c, lengths)
+    assert same_bits(o, o2) and same_bits(pool, pool2)
+    o, pool, err = run_decode(c)            # rows 0 and 2: NaN inputs, row 2 is padding
+    assert (o[2] == 0).all() and err == 0
+    assert torch.isfinite(pool.view(c["P"], -1)[1]).all()
+
+
+def test_pool_past_32_bits():
+    """A slot whose states lie beyond 2^31 elements of the pool."""
+    c = make(15, 2, 5, 5120, 1, 16, BF16, sdt=BF16, z=False)
+    P, per = 27000, 5120 * 16
+    assert (P - 1) * per > 2 ** 31
+    small = c["pool"].view(c["P"], per)
+    pool = torch.zeros(P, 5120, 16, dtype=BF16, device="cuda")
+    slots = [int(s) for s in c["slots"]]
+    far = [P - 1, 7]
+    for f, s in zip(far, slots):
+        pool[f] = small[s].view(5120, 16).cuda()
+    want, state, lim, slim, _ = plain(c)
+    out = torch.empty(2, 5, 5120, dtype=BF16, device="cuda")
+    idx = torch.tensor(far, dtype=torch.int32, device="cuda")
+    ssu.scan_prefill(cut(c["x"], 1), cut(c["dt"], 1), c["A"].cuda(), cut(c["B"], 1),
+                     cut(c["C"], 1), pool, out, D=c["D"].cuda(), dt_bias=c["bias"].cuda(),
+                     state_indices=idx)
+    torch.cuda.synchronize()
+    near(out.cpu(), want, lim, BF16, "out")
+    near(pool[far].cpu(), state[slots], slim[slots], BF16, "state")
+    one = torch.empty(2, 5120, dtype=BF16, device="cuda")
+    before = pool[far].clone()
+    ssu.scan_decode(cut(c["x"], 1)[:, 0].contiguous(), cut(c["dt"], 1)[:, 0].contiguous(),
+                    c["A"].cuda(), cut(c["B"], 1)[:, 0].contiguous(),
+                    cut(c["C"], 1)[:, 0].contiguous(), pool, one, state_indices=idx)
+    assert not torch.equal(pool[far], before)
+    assert int((pool != 0).flatten(1).any(1).sum()) == 2
+
+
+def test_long_row_in_a_graph_beside_another_stream():
+    """Segments over a cluster, captured by a first call and replayed, while the same call
+    runs on another stream with buffers of its own."""
+    c = make(16, 1, 3000, 40, 1, 16, BF16)
+    want, pool, _ = run(c)
+    t = {k: cut(c[k], 1) for k in ("x", "dt", "B", "C", "z")}
+    A, D, bias, sl = (c[k].cuda() for k in ("A", "D", "bias", "slots"))
+    pools = [c["pool"].cuda() for _ in range(2)]
+    outs = [torch.zeros(1, 3000, 40, dtype=BF16, device="cuda") for _ in range(2)]
+    s, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def go(i, stream=None):
+        ssu.scan_prefill(t["x"], t["dt"], A, t["B"], t["C"], pools[i], outs[i], D=D, z=t["z"],
+                         dt_bias=bias, state_indices=sl, P=c["P"], stream=stream)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        go(0)
+    graph.replay()
+    go(1, s2)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert same_bits(outs[i], want) and same_bits(pools[i], pool)

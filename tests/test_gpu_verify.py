@@ -290,3 +290,32 @@ def test_speculative_step_equals_single_tokens(form):
         per = strides[0]
         assert same_bits(conv[s * per:(s + 1) * per], one_conv[s * per:(s + 1) * per])
         assert torch.allclose(pool[s], one_pool[s], rtol=1e-5, atol=1e-5)
+
+
+def test_rows_past_32_bits():
+    """Distributions that lie beyond 2^31 elements: a chain's and a tree's last rows."""
+    b, T, V = 140, 128, 131072
+    assert b * T * V > 2 ** 31
+    p = torch.zeros(b, T, V, dtype=F16, device="cuda")
+    i = torch.arange(b, device="cuda")
+    hot = (i * 911 + 17) % V
+    for t in (0, T - 1):
+        p[i, t, hot] = 0.75
+        p[i, t, (hot + 5) % V] = 0.25
+    p[:, 1:T - 1, 3] = 1.0
+    tokens = torch.full((b, T), 3, dtype=I32, device="cuda")
+    tokens[:, 1] = hot.int()
+    u = torch.full((b, T), 0.5, device="cuda")
+    us = torch.full((b,), 0.9, device="cuda")
+    acc, nxt = torch.zeros(b, dtype=I32, device="cuda"), torch.zeros(b, dtype=I32, device="cuda")
+    ssu.spec_verify(tokens, p, u, us, acc, nxt)
+    # position 0 takes its token (0.5 < 0.75), positions 1.. token 3 (0.5 < 1): all accepted,
+    # and 0.9 of the last row's mass lies on its second token
+    low = torch.minimum(hot, (hot + 5) % V)
+    want = torch.where(low == hot, (hot + 5) % V, hot)
+    assert (acc == T).all() and torch.equal(nxt.long(), want)
+    parents = torch.arange(-1, T - 1, dtype=I32, device="cuda").expand(b, T).contiguous()
+    nodes = torch.zeros(b, T, dtype=I32, device="cuda")
+    ssu.spec_verify(tokens, p, u, us, acc, nxt, parent_ids=parents, accepted_node_ids=nodes)
+    assert (acc == T).all() and torch.equal(nxt.long(), want)
+    assert torch.equal(nodes, torch.arange(T, dtype=I32, device="cuda").expand(b, T))
