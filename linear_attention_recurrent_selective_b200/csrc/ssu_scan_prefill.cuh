@@ -9,12 +9,12 @@
 // Bound: the special-function unit (16 exponentials a clock and SM, so one clock per
 // (token, channel) and SM at N = 16), ahead of memory (x, dt, z, out: 8 bytes).
 //
-// Measured (B200, bfloat16, 5120 channels, 16 states): 16 full rows of 512 tokens 265 us, 16
-// ragged ones 148 us, against 97 us (full: 192) for the special-function operations alone
-// (16 decays, 3 for the softplus, 2 for the gate); that unit is 73 % busy and issue slots 65 %.
+// Measured (B200, bfloat16, 5120 channels, 16 states): 16 full rows of 512 tokens 263 us, 16
+// ragged ones 146 us, against 88 us (full: 174) for the special-function operations alone
+// (16 decays, 1 for the softplus, 2 for the gate); that unit is 69 % busy and issue slots 65 %.
 // Without the decays' exponentials the full rows take 253 of then 286 us, without softplus
 // and gate 233, without the exchanges between lanes 251, and B and C cost nothing: what
-// bounds it is the sum of what a warp issues. One row of 4099 tokens of 1000 channels: 80 us
+// bounds it is the sum of what a warp issues. One row of 4099 tokens of 1000 channels: 79 us
 // in 32 segments (770 us in one).
 //
 // Layout: a lane holds 8 states of a channel, kL = N / 8 lanes a channel; a CTA takes a block
@@ -104,9 +104,9 @@ __device__ __forceinline__ void copy16(void *dst, const void *src, int bytes)
 
 constexpr int log2_of(int n) { return n <= 1 ? 0 : 1 + log2_of(n / 2); }
 
-// Bring kTok rows of kRow (a power of two) elements (of which the first `left` exist) of tokens t0.. into
-// shared memory, zeros beyond token t1 and element `left`. Row t starts at element
-// t * ld of src.
+// Bring kTok rows of kRow (a power of two) elements (of which the first `left` exist) of
+// tokens t0.. into shared memory, zeros beyond token t1 and element `left`. Row t starts at
+// element t * ld of src.
 template <int kThreads, int kTok, int kRow>
 __device__ __forceinline__ void fetch_rows(uint8_t *dst, const void *src, int es, int64_t ld,
                                            int left, int t0, int t1, bool vec, int tid)
