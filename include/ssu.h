@@ -272,7 +272,8 @@ int ssu_conv_decode(const void *xbc, int x_dtype, const void *conv_weight,
  *                update_state == 0): the inputs before node t are its ancestors (parent, grandparent, ...), then
  *                the window. A node with a parent outside [-1, L_b) among its width-1
  *                nearest ancestors gets outputs 0 and SSU_FLAG_TREE.
- *   width 1..16. Padding rows write zeros to the outputs at every t < T.
+ *   width 1..16; batch, T and the channels together up to 2^30. Padding rows write zeros to
+ *   the outputs at every t < T.
  * xbc must not overlap the outputs. One launch.
  */
 int ssu_conv_prefill(const void *xbc, int x_dtype, int64_t xbc_stride, const void *conv_weight,
@@ -320,7 +321,7 @@ int ssu_conv_replay(const void *xbc, int x_dtype, int64_t xbc_stride, void *conv
  *            0: the pool is only read (needs out)
  * A speculative draft is verified with update_state = 0 and committed by a second call with
  * out = NULL and the accepted lengths as context_lengths. Padding rows write zeros to out at
- * every t < T. dstate in {8, 16, 32, 64, 128, 256}.
+ * every t < T. dstate in {8, 16, 32, 64, 128, 256}; batch, T and channels up to 2^30.
  */
 int scan_prefill(const void *x, int x_dtype, int64_t x_stride, const void *dt, int dt_dtype,
                  int64_t dt_stride, const float *A, const void *B, const void *C, int bc_dtype,
@@ -379,6 +380,7 @@ int scan_decode(const void *x, int x_dtype, int64_t x_stride, const void *dt, in
  *                    for L_b == 0 and for a tree without a root)
  *   accepted_node_ids [batch, max_accept_len] int32 (optional, trees only): the path, -1
  *                    beyond it
+ * Nothing is written when T == 0 (the Python binding refuses it).
  * Flags: SSU_FLAG_TOKEN (a drafted token outside [0, vocab), never accepted), SSU_FLAG_TREE
  * (a parent outside [-1, L_b), or no root: the node is never accepted), SSU_FLAG_NO_MASS
  * (p itself holds no mass: next token -1), and the length flags. One launch.

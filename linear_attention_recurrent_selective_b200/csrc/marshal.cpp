@@ -74,6 +74,13 @@ struct Reader {
         }
         return v;
     }
+    int64_t size()                              // -1: not given
+    {
+        const int64_t v = integer(-1);
+        if (v < 0 && args[-1] != Py_None)
+            refuse("a size is negative: " + std::to_string(v));
+        return v;
+    }
     int32_t int32(int64_t none)
     {
         const int64_t v = integer(none);
@@ -283,7 +290,7 @@ PyObject *conv_prefill(PyObject *, PyObject *const *args, Py_ssize_t n)
         const int32_t width = r.int32(0);
         const int64_t cs = r.integer(0), cc = r.integer(0), ck = r.integer(0);
         const int silu = r.truth(), update = r.truth();
-        const int64_t P = r.integer(-1);
+        const int64_t P = r.size();
         if (xbc.dim() != 3)
             refuse("xbc must be [batch, T, channels]");
         const int64_t b = xbc.size(0), T = xbc.size(1), ch = xbc.size(2);
@@ -318,7 +325,7 @@ PyObject *conv_replay(PyObject *, PyObject *const *args, Py_ssize_t n)
         const Tensor *const ids = r.optional("accepted_node_ids");
         const Tensor *const err = r.optional("err_flags");
         const int32_t width = r.int32(0);
-        const int64_t cs = r.integer(0), cc = r.integer(0), ck = r.integer(0), P = r.integer(-1);
+        const int64_t cs = r.integer(0), cc = r.integer(0), ck = r.integer(0), P = r.size();
         if (xbc.dim() != 3 || (ids && ids->dim() != 2))
             refuse("xbc must be [batch, T, channels], accepted_node_ids [batch, maxAcceptLen]");
         const int64_t b = xbc.size(0), T = xbc.size(1), ch = xbc.size(2);
@@ -370,8 +377,8 @@ struct Scan {
         N = B->size(lead + 1);
         per = G * N;
         softplus = r.truth();
-        stride = r.integer(-1);
-        int64_t slots = r.integer(-1);
+        stride = r.size();
+        int64_t slots = r.size();
         active = r.int32(b);
         same_type(z, *x, "z", "x");
         same_type(C, *B, "C", "B");
@@ -469,6 +476,8 @@ PyObject *spec_verify_(PyObject *, PyObject *const *args, Py_ssize_t n)
             refuse("target_probs must be [batch, T, vocab], accepted_node_ids [batch, "
                    "maxAcceptLen]");
         const int64_t b = p.size(0), T = p.size(1), V = p.size(2);
+        if (T == 0)
+            refuse("target_probs has no tokens: there is no row to draw from");
         const int32_t active = r.int32(b);
         same_type(q, p, "draft_probs", "target_probs");
         const int64_t most = nodes ? nodes->size(1) : 0;

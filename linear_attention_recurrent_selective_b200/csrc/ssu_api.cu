@@ -82,6 +82,10 @@ int check_conv_pool(int64_t slot_stride, int64_t stride_c, int64_t stride_k, int
     return SSU_OK;
 }
 
+// Rows, tokens of a row and channels of the entries below: headroom for the kernels' 32-bit
+// counters, which run past them by up to a tile.
+constexpr int32_t kMostRow = 1 << 30;
+
 int check_scan(int x_dtype, int64_t x_stride, int dt_dtype, int64_t dt_stride, int bc_dtype,
                int64_t B_stride, int64_t C_stride, bool gated, int64_t z_stride, int state_dtype,
                int64_t slot_stride, int32_t P, const int32_t *idx, int32_t batch, int32_t active,
@@ -93,6 +97,8 @@ int check_scan(int x_dtype, int64_t x_stride, int dt_dtype, int64_t dt_stride, i
     int rc = check_sizes(state_dtype, slot_stride, P, idx, batch, active, channels, groups, 1, N);
     if (rc != SSU_OK)
         return rc;
+    if (channels > kMostRow || batch > kMostRow)
+        return SSU_ERR_SHAPE;
     const int64_t bc = (int64_t)groups * N;
     if (x_stride < channels || dt_stride < channels || (gated && z_stride < channels) ||
         B_stride < bc || C_stride < bc)
@@ -377,12 +383,12 @@ int ssu_conv_prefill(const void *xbc, int x_dtype, int64_t xbc_stride, const voi
 {
     if (!valid_dtype(x_dtype))
         return SSU_ERR_DTYPE;
-    if (batch < 0 || active_batch < 0 || active_batch > batch || P < 0 || T < 0)
+    if (batch < 0 || active_batch < 0 || active_batch > batch || P < 0 || T < 0 || T > kMostRow)
         return SSU_ERR_SHAPE;
     if (x_dim <= 0 || bc_dim < 0)
         return SSU_ERR_SHAPE;
     const int64_t cd = (int64_t)x_dim + 2 * (int64_t)bc_dim;
-    if (cd > 0x7fffffffLL || xbc_stride < cd)
+    if (cd > kMostRow || batch > kMostRow || xbc_stride < cd)
         return SSU_ERR_SHAPE;
     int rc = check_conv_pool(conv_slot_stride, conv_stride_c, conv_stride_k, cd, width);
     if (rc != SSU_OK)
@@ -432,9 +438,10 @@ int ssu_conv_replay(const void *xbc, int x_dtype, int64_t xbc_stride, void *conv
 {
     if (!valid_dtype(x_dtype))
         return SSU_ERR_DTYPE;
-    if (batch < 0 || active_batch < 0 || active_batch > batch || P < 0 || T < 0)
+    if (batch < 0 || active_batch < 0 || active_batch > batch || P < 0 || T < 0 || T > kMostRow)
         return SSU_ERR_SHAPE;
-    if (conv_dim <= 0 || xbc_stride < conv_dim || (accepted_node_ids && max_accept_len < 0))
+    if (conv_dim <= 0 || conv_dim > kMostRow || xbc_stride < conv_dim ||
+        (accepted_node_ids && max_accept_len < 0))
         return SSU_ERR_SHAPE;
     int rc = check_conv_pool(conv_slot_stride, conv_stride_c, conv_stride_k, conv_dim, width);
     if (rc != SSU_OK)
@@ -474,7 +481,7 @@ int scan_prefill(const void *x, int x_dtype, int64_t x_stride, const void *dt, i
                  int32_t active_batch, int32_t T, int32_t channels, int32_t ngroups,
                  int32_t dstate, int dt_softplus, int32_t *err_flags, ssu_stream_t stream)
 {
-    if (T < 0)
+    if (T < 0 || T > kMostRow)
         return SSU_ERR_SHAPE;
     ssu::ScanArgs a = {};
     int rc = check_scan(x_dtype, x_stride, dt_dtype, dt_stride, bc_dtype, B_stride, C_stride,
@@ -535,7 +542,7 @@ int spec_verify(const int32_t *tokens, const void *target_probs, const void *dra
 {
     if (!valid_dtype(p_dtype))
         return SSU_ERR_DTYPE;
-    if (batch < 0 || active_batch < 0 || active_batch > batch || T < 0)
+    if (batch < 0 || active_batch < 0 || active_batch > batch || T < 0 || T > kMostRow)
         return SSU_ERR_SHAPE;
     if (vocab <= 0 || vocab > (1 << 30) || target_stride < vocab)
         return SSU_ERR_SHAPE;

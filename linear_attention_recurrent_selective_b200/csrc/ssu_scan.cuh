@@ -148,7 +148,9 @@ __device__ __forceinline__ void store_states(void *pool, int dtype, int64_t at, 
     }
 }
 
-// The rows A[d, :] times log2(e), so that a decay is one exp2 of a product.
+// The rows A[d, :] times log2(e), so that a decay is one exp2 of a product. A rate of -inf (a
+// state that forgets at once) becomes the lowest finite one: it decays by the same 0 over any
+// step, and a step of 0, which tokens behind the row's last one are given, is no NaN.
 template <int kS>
 __device__ __forceinline__ void load_decay_rates(const float *A, int64_t at, float (&r)[kS])
 {
@@ -160,6 +162,9 @@ __device__ __forceinline__ void load_decay_rates(const float *A, int64_t at, flo
         r[i + 1] = v.y * kLog2e;
         r[i + 2] = v.z * kLog2e;
         r[i + 3] = v.w * kLog2e;
+#pragma unroll
+        for (int e = i; e < i + 4; ++e)
+            r[e] = r[e] < -3.402823466e38f ? -3.402823466e38f : r[e];      // (a NaN stays one)
     }
 }
 

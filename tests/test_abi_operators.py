@@ -95,6 +95,22 @@ def test_scan_outputs_and_empty_calls(L):
     assert call(L.scan_decode, DEC, active=0, **nulls) == 0
 
 
+def test_sizes_near_the_counters_range(L):
+    big = 2 ** 30 + 1
+    assert call(L.ssu_conv_prefill, CONV, T=big) == 2
+    assert call(L.ssu_conv_prefill, CONV, batch=big, active=1) == 2
+    wide = dict(ld=2 ** 31, cs=2 ** 34)
+    assert call(L.ssu_conv_prefill, CONV, xd=2 ** 30 - 1, bc=1, **wide) == 2
+    assert call(L.ssu_conv_replay, COMMIT, ch=big, **wide) == 2
+    assert call(L.ssu_conv_replay, COMMIT, T=big) == 2
+    assert call(L.scan_prefill, PRE, T=big) == 2
+    rows = dict(ch=big, ldx=2 ** 31, lddt=2 ** 31, ldz=2 ** 31, stride=2 ** 36)
+    for fn, good in ((L.scan_prefill, PRE), (L.scan_decode, DEC)):
+        assert call(fn, good, **rows) == 2
+        assert call(fn, good, batch=big, active=1) == 2
+    assert call(L.spec_verify, VERIFY, T=big) == 2
+
+
 VERIFY = dict(tok=P16, p=P16, q=P16, dt=0, ldp=32768, ldq=32768, u=P16, us=P16, ctx=None,
               par=None, idx=None, acc=P16, nxt=P16, ids=None, most=0, batch=64, active=64, T=5,
               V=32768, err=None, stream=None)

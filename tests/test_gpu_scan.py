@@ -399,3 +399,28 @@ def test_long_row_in_a_graph_beside_another_stream():
     torch.cuda.synchronize()
     for i in range(2):
         assert same_bits(outs[i], want) and same_bits(pools[i], pool)
+
+
+@pytest.mark.parametrize("T,ch,N", [(1, 72, 8), (37, 72, 16), (45, 40, 128), (300, 16, 16),
+                                    (1100, 16, 64)])
+def test_rates_of_minus_infinity(T, ch, N):
+    """A state that forgets at once holds the last token's input, as with any rate whose decay
+    is 0 in fp32, whatever the tokens that a tile holds behind the row."""
+    c = make(T + N, 2, T, ch, 1, N, BF16)
+    hit = torch.rand(ch, N, generator=po.generator(9)) < 0.3
+    c["A"] = torch.where(hit, torch.tensor(-1e30), c["A"])
+    lengths = torch.tensor([T, max(T - 2, 1)], dtype=torch.int32)
+    want = run(c, lengths), run_decode(c)
+    c["A"] = torch.where(hit, torch.tensor(float("-inf")), c["A"])
+    for got, ref in zip((run(c, lengths), run_decode(c)), want):
+        assert torch.isfinite(ref[1]).all() and got[2] == ref[2]
+        assert same_bits(got[0], ref[0]) and same_bits(got[1], ref[1])
+
+
+def test_negative_sizes_are_refused():
+    c = make(1, 2, 4, 32, 1, 16, BF16)
+    args = [cut(c["x"], 1), cut(c["dt"], 1), c["A"].cuda(), cut(c["B"], 1), cut(c["C"], 1),
+            c["pool"].cuda(), torch.empty(2, 4, 32, dtype=BF16, device="cuda")]
+    for kw in (dict(P=-1), dict(P=c["P"], slot_stride=-1)):
+        with pytest.raises(ValueError):
+            ssu.scan_prefill(*args, **kw)

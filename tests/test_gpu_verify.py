@@ -223,6 +223,14 @@ def test_refusals():
             ssu.spec_verify(**{**ok, **kw})
 
 
+def test_no_tokens_are_refused():
+    none = dict(dtype=F32, device="cuda")
+    acc, nxt = torch.zeros(2, dtype=I32, device="cuda"), torch.zeros(2, dtype=I32, device="cuda")
+    with pytest.raises(ValueError):
+        ssu.spec_verify(torch.empty(2, 0, dtype=I32, device="cuda"), torch.empty(2, 0, 40, **none),
+                        torch.empty(2, 0, **none), torch.empty(2, **none), acc, nxt)
+
+
 # ---------------------------------------------------------------- the operators together
 
 def layer(seed, b, P, H, G, Dm, N, W):
