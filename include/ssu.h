@@ -380,7 +380,8 @@ int scan_decode(const void *x, int x_dtype, int64_t x_stride, const void *dt, in
  *                    for L_b == 0 and for a tree without a root)
  *   accepted_node_ids [batch, max_accept_len] int32 (optional, trees only): the path, -1
  *                    beyond it
- * Nothing is written when T == 0 (the Python binding refuses it).
+ * Nothing is written when T == 0 (the Python binding refuses it). The outputs overlap no
+ * input.
  * Flags: SSU_FLAG_TOKEN (a drafted token outside [0, vocab), never accepted), SSU_FLAG_TREE
  * (a parent outside [-1, L_b), or no root: the node is never accepted), SSU_FLAG_NO_MASS
  * (p itself holds no mass: next token -1), and the length flags. One launch.

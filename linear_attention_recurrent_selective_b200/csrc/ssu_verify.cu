@@ -18,10 +18,11 @@
 // Bound: memory for many rows (one row of p and at most one of q per sequence), latency
 // for one: a few dependent loads find the row, then it is streamed once.
 //
-// Measured (B200): 64 sequences of 4 drafted tokens over 2^17 tokens in fp32 20.5 us, of which
+// Measured (B200): 64 sequences of 4 drafted tokens over 2^17 tokens in fp32 18.9 us, of which
 // the rows' sums are 12.5 (0.79 of the copy rate), finding the row and the clusters' meeting
-// 6 and the drawn token 1.7; one sequence over 65537 tokens in bfloat16 7.6 us; 16 trees of
-// 128 nodes over 32768 tokens 10.7 us. Sums as pairs of floats instead of doubles: 33.7 us
+// 4.7 (6.2 where a length or an index was waited for before the tokens) and the drawn token
+// 1.7; one sequence over 65537 tokens in bfloat16 7.2 us; 16 trees of 128 nodes over 32768
+// tokens 10.3 us. Sums as pairs of floats instead of doubles: 33.7 us
 // against 27.3 for the same loop.
 //
 // Layout: a cluster of CTAs per sequence. Every CTA walks the chain or tree itself (a few
@@ -398,21 +399,26 @@ verify_kernel(const __grid_constant__ VerifyArgs a)
     const bool report = rank == 0 && a.err;
     cluster.barrier_arrive();         // waited for before another CTA's memory is written
 
-    const bool pad = a.idx && a.idx[b] < 0;
-    int L = a.T;
-    if (a.ctx && !pad) {
-        L = a.ctx[b];
-        if (report && tid == 0 && (L < 0 || L > a.T))
-            atomicOr(a.err, L < 0 ? SSU_FLAG_NEGATIVE_LENGTH : SSU_FLAG_CONTEXT_RANGE);
-        L = L < 0 ? 0 : (L > a.T ? a.T : L);
-    }
     const E *const rows = static_cast<const E *>(a.p) + (int64_t)b * a.T * a.ldp;
     const E *const drafts =
         a.q ? static_cast<const E *>(a.q) + (int64_t)b * (a.T - 1) * a.ldq : nullptr;
     const int32_t *const tokens = a.tokens + (int64_t)b * a.T;
     const float *const u = a.u + (int64_t)b * a.T;
+    const int32_t *const par = a.parents ? a.parents + (int64_t)b * a.T : nullptr;
+    // all loads that depend on no other are in flight before the first is waited for
+    const int slot = a.idx ? a.idx[b] : 0;
+    const int len = a.ctx ? a.ctx[b] : a.T;
     const float us = a.u_sample[b];
     const int most = a.nodes ? a.max_accept : a.T;
+    const int ahead = par ? 0 : 1;                      // a chain's position t checks token t + 1
+    const bool mine = tid + ahead < a.T;
+    const int x0 = mine ? tokens[tid + ahead] : 0;
+    const int up0 = mine && par ? par[tid] : -1;
+    const float u0 = mine ? u[tid] : 0.f;
+    const bool pad = slot < 0;
+    if (report && tid == 0 && !pad && (len < 0 || len > a.T))
+        atomicOr(a.err, len < 0 ? SSU_FLAG_NEGATIVE_LENGTH : SSU_FLAG_CONTEXT_RANGE);
+    const int L = len < 0 ? 0 : (len > a.T ? a.T : len);
 
     // ---- which tokens are accepted
     if (tid == 0) {
@@ -422,15 +428,16 @@ verify_kernel(const __grid_constant__ VerifyArgs a)
         s.n = 0;
     }
     __syncthreads();
-    if (!pad && L > 0 && !a.parents) {
+    if (!pad && L > 0 && !par) {
         for (int t = tid; t + 1 < L; t += kThreads) {
-            const int x = tokens[t + 1];
+            const int x = t == tid ? x0 : tokens[t + 1];
+            const float ut = t == tid ? u0 : u[t];
             const bool in = x >= 0 && x < a.V;
             bool ok = false;
             if (in) {
                 const float p = mass_of(to_f32<E>(rows[t * a.ldp + x]));
                 const float q = drafts ? mass_of(to_f32<E>(drafts[t * a.ldq + x])) : 1.f;
-                ok = (double)u[t] * (double)q < (double)p;
+                ok = (double)ut * (double)q < (double)p;
             } else if (report) {
                 atomicOr(a.err, SSU_FLAG_TOKEN);
             }
@@ -447,13 +454,10 @@ verify_kernel(const __grid_constant__ VerifyArgs a)
             }
         }
     } else if (!pad && L > 0) {
-        const int32_t *const par = a.parents + (int64_t)b * a.T;
-        int up = -1, x = 0;
+        const int up = up0, x = x0;
         float p = 0.f;
         if (tid < L) {
-            up = par[tid];
-            x = tokens[tid];
-            s.u[tid] = u[tid];
+            s.u[tid] = u0;
             const bool child = up >= 0 && up < L;
             if (up == -1)
                 atomicMin(&s.root, tid);
@@ -520,7 +524,7 @@ verify_kernel(const __grid_constant__ VerifyArgs a)
 
     // ---- the next token, by whole vectors where both rows allow it
     constexpr int V = Vec16<E>::kElems;
-    const bool rejected = !a.parents && n < L;
+    const bool rejected = !par && n < L;
     const E *const row = rows + s.end * a.ldp;
     const E *const sub = rejected && drafts ? drafts + s.end * a.ldq : nullptr;
     const int skew = (int)(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(E));
