@@ -13,12 +13,12 @@
 // W + 3 multiply-adds and two special-function operations (the sigmoid); windows are
 // touched once per row.
 //
-// Measured (B200, bfloat16, 5376 channels, width 4): 16 ragged rows of up to 512 tokens 26.6
+// Measured (B200, bfloat16, 5376 channels, width 4): 16 ragged rows of up to 512 tokens 26.0
 // us, 16 full ones 39 us (0.71 of the copy rate; a full wave's strips end together, and the
 // sigmoid's two special-function operations an element take half of that time); one token of
 // each of 256 rows 5.6 us (0.61); draft trees of 16 x 128 nodes in half precision 18.5 us
 // (0.37: a CTA loads, walks, computes and stores one after the other, in little over one
-// wave); the commit of 64 rows 3.3 us, of which a launch alone is about 2.5.
+// wave); the commit of 64 rows 3.1 us, of which a launch alone is about 2.5.
 //
 // Layout: a thread owns VEC neighbouring channels (one access of a row; one channel where
 // rows or segments are not aligned) over a strip of up to kStrip tokens, and slides the
@@ -310,13 +310,14 @@ __device__ __forceinline__ OutSeg<E> out_seg(const ConvPrefillArgs &a, int64_t b
     return OutSeg<E>{static_cast<E *>(base) + b * a.T * dim + c, dim};
 }
 
-// A row's clamped length; the row's first thread reports a length outside [0, T].
-__device__ __forceinline__ int row_length(const int32_t *len, int b, int T, int over_flag,
-                                          bool report, int32_t *err)
+// A row's length as given, asked for before its slot is looked at so that the two loads share
+// one round trip; then clamped, where the row's first thread reports one outside [0, T].
+__device__ __forceinline__ int given_length(const int32_t *len, int64_t b, int T)
 {
-    if (!len)
-        return T;
-    const int L = len[b];
+    return len ? len[b] : T;
+}
+__device__ __forceinline__ int row_length(int L, int T, int over_flag, bool report, int32_t *err)
+{
     if (report && err && (L < 0 || L > T))
         atomicOr(err, L < 0 ? SSU_FLAG_NEGATIVE_LENGTH : over_flag);
     return L < 0 ? 0 : (L > T ? T : L);
@@ -336,6 +337,7 @@ conv_prefill_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups,
         return;
     const int c0 = g * VEC, t0 = strip * kStrip;
     const bool first = strip == 0 && g == 0;
+    const int len = given_length(a.ctx, b, a.T);
     const int slot = a.idx ? a.idx[b] : (int)b;
     if (slot >= a.P) {                          // caller bug: skip the row and report it
         if (first && a.err)
@@ -349,7 +351,7 @@ conv_prefill_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups,
             store_floats<E, VEC>(out.p + t * out.ld, zero);
         return;
     }
-    const int L = row_length(a.ctx, (int)b, a.T, SSU_FLAG_CONTEXT_RANGE, first, a.err);
+    const int L = row_length(len, a.T, SSU_FLAG_CONTEXT_RANGE, first, a.err);
     const int t1 = min(t0 + kStrip, L);
     if (t0 >= L)
         return;
@@ -455,6 +457,7 @@ conv_stream_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups, 
         return;
     const int c0 = g * VEC, t0 = strip * kStrip;
     const bool first = strip == 0 && g == 0;
+    const int len = given_length(a.ctx, b, a.T);
     const int slot = a.idx ? a.idx[b] : (int)b;
     if (slot >= a.P) {                          // caller bug: skip the row and report it
         if (first && a.err)
@@ -468,7 +471,7 @@ conv_stream_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups, 
             store_floats<E, VEC>(out.p + t * out.ld, zero);
         return;
     }
-    const int L = row_length(a.ctx, (int)b, a.T, SSU_FLAG_CONTEXT_RANGE, first, a.err);
+    const int L = row_length(len, a.T, SSU_FLAG_CONTEXT_RANGE, first, a.err);
     const int t1 = min(t0 + kStrip, L);
     if (t0 >= L)
         return;
@@ -573,17 +576,22 @@ conv_token_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups)
     const int64_t b0 = id / groups * kRows;
     if (b0 >= a.active)
         return;
-    int slot[kRows];
+    int slot[kRows], len[kRows];
     bool live[kRows];
     Chunk<E, VEC> x[kRows];
     E tap[kRows][W - 1][VEC];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
         const int64_t b = b0 + r;
+        len[r] = b < a.active ? given_length(a.ctx, b, 1) : 0;
         slot[r] = b < a.active ? (a.idx ? a.idx[b] : (int)b) : a.P;
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        const int64_t b = b0 + r;
         live[r] = slot[r] >= 0 && slot[r] < a.P;
         if (live[r])
-            live[r] = row_length(a.ctx, (int)b, 1, SSU_FLAG_CONTEXT_RANGE, g == 0, a.err) == 1;
+            live[r] = row_length(len[r], 1, SSU_FLAG_CONTEXT_RANGE, g == 0, a.err) == 1;
         else if (b < a.active && slot[r] >= 0 && g == 0 && a.err)
             atomicOr(a.err, SSU_FLAG_INDEX_RANGE);      // caller bug: skip and report
     }
@@ -655,6 +663,7 @@ conv_prefill_any_kernel(const __grid_constant__ ConvPrefillArgs a, const int cha
         return;
     const int t0 = strip * kStrip, W = a.width;
     const bool first = strip == 0 && c == 0;
+    const int len = given_length(a.ctx, b, a.T);
     const int slot = a.idx ? a.idx[b] : (int)b;
     if (slot >= a.P) {
         if (first && a.err)
@@ -667,7 +676,7 @@ conv_prefill_any_kernel(const __grid_constant__ ConvPrefillArgs a, const int cha
             out.p[t * out.ld] = narrow<E>(0.f);
         return;
     }
-    const int L = row_length(a.ctx, (int)b, a.T, SSU_FLAG_CONTEXT_RANGE, first, a.err);
+    const int L = row_length(len, a.T, SSU_FLAG_CONTEXT_RANGE, first, a.err);
     const int t1 = min(t0 + kStrip, L);
     if (t0 >= L)
         return;
@@ -705,6 +714,7 @@ conv_tree_kernel(const __grid_constant__ ConvPrefillArgs a, const int blocks, co
     const int b = blockIdx.x / blocks, tid = threadIdx.x;
     const int c0 = (blockIdx.x % blocks) * kCh, channels = a.x_dim + 2 * a.bc_dim;
     const bool first = blockIdx.x % blocks == 0 && tid == 0;
+    const int len = given_length(a.ctx, b, a.T);
     const int slot = a.idx ? a.idx[b] : b;
     if (slot >= a.P) {                          // caller bug: skip the row and report it
         if (first && a.err)
@@ -733,7 +743,7 @@ conv_tree_kernel(const __grid_constant__ ConvPrefillArgs a, const int blocks, co
             store(t, zero);
         return;
     }
-    const int L = row_length(a.ctx, b, a.T, SSU_FLAG_CONTEXT_RANGE, first, a.err);
+    const int L = row_length(len, a.T, SSU_FLAG_CONTEXT_RANGE, first, a.err);
     if (L == 0)
         return;
 
@@ -860,6 +870,8 @@ conv_replay_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups, 
 {
     const int b = blockIdx.x / blocks, part = blockIdx.x % blocks;
     const bool first = part == 0 && threadIdx.x == 0;
+    const int most = a.nodes ? a.max_accept : a.T;
+    const int len = given_length(a.ctx, b, most);
     const int slot = a.idx ? a.idx[b] : b;
     if (slot < 0)
         return;
@@ -868,8 +880,7 @@ conv_replay_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups, 
             atomicOr(a.err, SSU_FLAG_INDEX_RANGE);
         return;
     }
-    const int most = a.nodes ? a.max_accept : a.T;
-    const int k = row_length(a.ctx, b, most, SSU_FLAG_ACCEPTED_RANGE, first, a.err);
+    const int k = row_length(len, most, SSU_FLAG_ACCEPTED_RANGE, first, a.err);
     if (k == 0)
         return;
     const int32_t *ids = a.nodes ? a.nodes + (int64_t)b * a.max_accept : nullptr;

@@ -208,10 +208,10 @@ __device__ __forceinline__ void widen_rows(float *dst, const uint8_t *raw, int d
 // Length used to order the rows: padding and out-of-range rows do (almost) no work.
 __device__ __forceinline__ int sched_len(const ScanArgs &a, int b)
 {
+    const int L = a.ctx ? a.ctx[b] : a.T;           // (one round trip for both)
     const int slot = a.idx ? a.idx[b] : b;
     if (slot < 0 || slot >= a.P)
         return 0;
-    const int L = a.ctx ? a.ctx[b] : a.T;
     return L < 0 ? 0 : (L > a.T ? a.T : L);
 }
 
@@ -438,6 +438,7 @@ scan_prefill_kernel(const __grid_constant__ ScanArgs a, const int blocks, const 
     blk.g = unit % blocks / of_group;
     blk.d0 = blk.g * per + unit % blocks % of_group * kCh;
     blk.n = min(kCh, (blk.g + 1) * per - blk.d0);
+    const int len = a.ctx ? a.ctx[b] : a.T;                 // (in one round trip with the slot)
     const int slot = a.idx ? a.idx[b] : b;
     const bool first = unit % blocks == 0 && part == 0 && threadIdx.x == 0;
     if (slot >= a.P) {                                      // caller bug: skip and report
@@ -454,13 +455,9 @@ scan_prefill_kernel(const __grid_constant__ ScanArgs a, const int blocks, const 
         }
         return;
     }
-    int L = a.T;
-    if (a.ctx) {
-        L = a.ctx[b];
-        if (first && a.err && (L < 0 || L > a.T))
-            atomicOr(a.err, L < 0 ? SSU_FLAG_NEGATIVE_LENGTH : SSU_FLAG_CONTEXT_RANGE);
-        L = L < 0 ? 0 : (L > a.T ? a.T : L);
-    }
+    if (first && a.err && (len < 0 || len > a.T))
+        atomicOr(a.err, len < 0 ? SSU_FLAG_NEGATIVE_LENGTH : SSU_FLAG_CONTEXT_RANGE);
+    const int L = len < 0 ? 0 : (len > a.T ? a.T : len);
     if (L == 0)
         return;
 
