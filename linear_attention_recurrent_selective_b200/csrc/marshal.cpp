@@ -147,6 +147,14 @@ const int32_t *indices(const Tensor *t, const char *name, std::initializer_list<
     return dense<const int32_t>(t, name, shape, ScalarType::Int);
 }
 
+// Lists of accepted nodes [rows, most]: a missing one is NULL, one of no columns is not. It has
+// no elements and torch no address for it, so it gets that of another tensor, never read.
+int32_t *node_lists(const Tensor *t, const char *name, int64_t rows, int64_t most, const Tensor &other)
+{
+    int32_t *const p = dense<int32_t>(t, name, {rows, most}, ScalarType::Int);
+    return t && !p ? static_cast<int32_t *>(other.data_ptr()) : p;
+}
+
 void same_type(const Tensor *t, const Tensor &as, const char *name, const char *other)
 {
     if (t && t->scalar_type() != as.scalar_type())
@@ -337,7 +345,7 @@ PyObject *conv_replay(PyObject *, PyObject *const *args, Py_ssize_t n)
         return fn(xbc.data_ptr(), code(xbc, "xbc"), ld, cp.p, cp.slot, cp.c, cp.k, width, cp.P,
                   indices(&acc, "accepted_lengths", {b}), indices(idx, "state_indices", {b}),
                   fit32(b, "batch"), active, fit32(T, "T"), fit32(ch, "channels"),
-                  indices(ids, "accepted_node_ids", {b, most}), fit32(most, "maxAcceptLen"),
+                  node_lists(ids, "accepted_node_ids", b, most, acc), fit32(most, "maxAcceptLen"),
                   dense<int32_t>(err, "err_flags", {1}, ScalarType::Int),
                   stream_of(stream, r.device));
     });
@@ -492,7 +500,7 @@ PyObject *spec_verify_(PyObject *, PyObject *const *args, Py_ssize_t n)
                   indices(idx, "state_indices", {b}),
                   dense<int32_t>(&acc, "accepted_lengths", {b}, ScalarType::Int),
                   dense<int32_t>(&nxt, "next_tokens", {b}, ScalarType::Int),
-                  dense<int32_t>(nodes, "accepted_node_ids", {b, most}, ScalarType::Int),
+                  node_lists(nodes, "accepted_node_ids", b, most, acc),
                   fit32(most, "maxAcceptLen"), fit32(b, "batch"), active, fit32(T, "T"),
                   fit32(V, "vocab"), dense<int32_t>(err, "err_flags", {1}, ScalarType::Int),
                   stream_of(stream, r.device));

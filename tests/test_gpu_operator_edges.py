@@ -1,0 +1,33 @@
+"""GPU tests of the calls at the edges of the convolution, scan and verification operators."""
+
+import pytest
+import torch
+
+from linear_attention_recurrent_selective_b200 import ssu
+from parity import same_bits
+
+pytestmark = pytest.mark.gpu
+
+I32 = torch.int32
+DEV = dict(device="cuda")
+
+
+# ---------------------------------------------------------------- empty lists of nodes
+
+def test_a_commit_of_an_empty_list_of_nodes_takes_nothing():
+    """accepted_node_ids of no columns bounds every length to zero."""
+    xbc, pool = torch.randn(2, 5, 8, **DEV), torch.randn(2, 8, 3, **DEV)
+    before, err = pool.clone(), torch.zeros(1, dtype=I32, **DEV)
+    acc, none = torch.tensor([2, 0], dtype=I32, **DEV), torch.empty(2, 0, dtype=I32, **DEV)
+    ssu.ssu_conv_replay(xbc, pool, acc, width=4, conv_strides=(24, 3, 1), accepted_node_ids=none,
+                        err_flags=err)
+    assert same_bits(pool, before) and int(err.item()) == ssu.FLAG_ACCEPTED_RANGE
+
+
+def test_a_verification_into_an_empty_list_of_nodes_is_refused():
+    p = torch.softmax(torch.randn(2, 3, 40, **DEV), -1)
+    tok, par = torch.zeros(2, 3, dtype=I32, **DEV), torch.full((2, 3), -1, dtype=I32, **DEV)
+    acc, nxt = torch.zeros(2, dtype=I32, **DEV), torch.zeros(2, dtype=I32, **DEV)
+    with pytest.raises(ssu.SSUError):
+        ssu.spec_verify(tok, p, torch.rand(2, 3, **DEV), torch.rand(2, **DEV), acc, nxt,
+                        parent_ids=par, accepted_node_ids=torch.empty(2, 0, dtype=I32, **DEV))
