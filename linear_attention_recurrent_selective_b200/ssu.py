@@ -290,12 +290,17 @@ def ssu_prefill(x, A, B, C, dt, state, out, *, dt_bias=None, D=None, z=None,
     return out
 
 
-def _node_ids(accepted_node_ids):
+def _node_ids(accepted_node_ids, other):
+    """(pointer, columns) of the lists of accepted nodes. Lists of no columns have no address,
+    which would read as no lists: they get that of the tensor ``other``, never read."""
     if accepted_node_ids is None:
         return None, 0
     if accepted_node_ids.dim() != 2:
         raise ValueError("accepted_node_ids must be [batch, maxAcceptLen]")
-    return _ptr(accepted_node_ids, "accepted_node_ids", torch.int32), accepted_node_ids.shape[1]
+    p = _ptr(accepted_node_ids, "accepted_node_ids", torch.int32)
+    if accepted_node_ids.shape[1] == 0:
+        p = _ptr(other, "accepted_lengths", torch.int32)
+    return p, accepted_node_ids.shape[1]
 
 
 def ssu_replay(state, stash, accepted_lengths, *, state_indices=None, active_batch=None,
@@ -315,7 +320,7 @@ def ssu_replay(state, stash, accepted_lengths, *, state_indices=None, active_bat
         _ptr(sdA, "stash dA", f32), _ptr(sU, "stash U", f32), _ptr(sB, "stash B", f32),
         _ptr(sdt, "stash dt", f32), _ptr(accepted_lengths, "accepted_lengths", torch.int32),
         _ptr(state_indices, "state_indices", torch.int32), batch, active, T, H, G, Dm, N,
-        *_node_ids(accepted_node_ids), _ptr(err_flags, "err_flags", torch.int32),
+        *_node_ids(accepted_node_ids, accepted_lengths), _ptr(err_flags, "err_flags", torch.int32),
         _stream(stream))
     _check("ssu_replay", rc)
 
@@ -590,7 +595,7 @@ def ssu_replay_layers(table, num_layers, like_state, like_stash, accepted_length
         _ptr(table, "layer table", torch.int64), num_layers, _dt(like_state, "state"), stride,
         P, _ptr(accepted_lengths, "accepted_lengths", torch.int32),
         _ptr(state_indices, "state_indices", torch.int32), batch, active, T, H, G, Dm, N,
-        *_node_ids(accepted_node_ids), _ptr(err_flags, "err_flags", torch.int32),
+        *_node_ids(accepted_node_ids, accepted_lengths), _ptr(err_flags, "err_flags", torch.int32),
         _stream(stream))
     _check("ssu_replay_layers", rc)
 

@@ -31,3 +31,19 @@ def test_a_verification_into_an_empty_list_of_nodes_is_refused():
     with pytest.raises(ssu.SSUError):
         ssu.spec_verify(tok, p, torch.rand(2, 3, **DEV), torch.rand(2, **DEV), acc, nxt,
                         parent_ids=par, accepted_node_ids=torch.empty(2, 0, dtype=I32, **DEV))
+
+
+def test_a_replay_of_an_empty_list_of_nodes_takes_nothing():
+    b, T, H, G, Dm, N = 2, 3, 2, 1, 8, 16
+    pool = torch.randn(b, H, Dm, N, **DEV)
+    stash = (torch.rand(b, T, H, **DEV), torch.randn(b, T, H, Dm, **DEV),
+             torch.randn(b, T, G, N, **DEV), torch.rand(b, T, H, **DEV))
+    acc, none = torch.tensor([2, 0], dtype=I32, **DEV), torch.empty(b, 0, dtype=I32, **DEV)
+    for layers in (False, True):
+        got, err = pool.clone(), torch.zeros(1, dtype=I32, **DEV)
+        if layers:
+            table = ssu.replay_layer_table([(got, stash)])
+            ssu.ssu_replay_layers(table, 1, got, stash, acc, accepted_node_ids=none, err_flags=err)
+        else:
+            ssu.ssu_replay(got, stash, acc, accepted_node_ids=none, err_flags=err)
+        assert same_bits(got, pool) and int(err.item()) == ssu.FLAG_ACCEPTED_RANGE
