@@ -149,7 +149,8 @@ const int32_t *indices(const Tensor *t, const char *name, std::initializer_list<
 
 // Lists of accepted nodes [rows, most]: a missing one is NULL, one of no columns is not. It has
 // no elements and torch no address for it, so it gets that of another tensor, never read.
-int32_t *node_lists(const Tensor *t, const char *name, int64_t rows, int64_t most, const Tensor &other)
+int32_t *node_lists(const Tensor *t, const char *name, int64_t rows, int64_t most,
+                    const Tensor &other)
 {
     int32_t *const p = dense<int32_t>(t, name, {rows, most}, ScalarType::Int);
     return t && !p ? static_cast<int32_t *>(other.data_ptr()) : p;
@@ -247,6 +248,16 @@ ssu_stream_t stream_of(PyObject *stream, int device)
     return reinterpret_cast<ssu_stream_t>((uintptr_t)v);
 }
 
+// Calls an entry point without the interpreter's lock, as ctypes does: a launch into a full
+// queue waits for the device, which may itself wait for a host function of another thread.
+template <typename Fn, typename... Args> int unlocked(Fn fn, Args... args)
+{
+    PyThreadState *const thread = PyEval_SaveThread();
+    const int rc = fn(args...);
+    PyEval_RestoreThread(thread);
+    return rc;
+}
+
 // Runs `body` (Reader, entry point, stream argument) and turns what it throws into a
 // Python exception.
 template <typename Fn, typename Body>
@@ -313,13 +324,15 @@ PyObject *conv_prefill(PyObject *, PyObject *const *args, Py_ssize_t n)
         const ConvPool cp = conv_pool(pool, xbc, ch, width, cs, cc, ck, P);
         const ScalarType type = xbc.scalar_type();
         const c10::cuda::CUDAGuard on((c10::DeviceIndex)r.device);
-        return fn(xbc.data_ptr(), code(xbc, "xbc"), ld, dense(&weight, "conv_weight", {ch, width}, type),
-                  dense(bias, "conv_bias", {ch}, type), cp.p, cp.slot, cp.c, cp.k, width, silu, cp.P,
-                  px, pB, pC, indices(idx, "state_indices", {b}),
-                  indices(len, "context_lengths", {b}), indices(parents, "parent_ids", {b, T}),
-                  update, fit32(b, "batch"), active, fit32(T, "T"), xd, bd,
-                  dense<int32_t>(err, "err_flags", {1}, ScalarType::Int),
-                  stream_of(stream, r.device));
+        return unlocked(
+            fn, xbc.data_ptr(), code(xbc, "xbc"), ld,
+            dense(&weight, "conv_weight", {ch, width}, type),
+            dense(bias, "conv_bias", {ch}, type), cp.p, cp.slot, cp.c, cp.k, width, silu,
+            cp.P, px, pB, pC, indices(idx, "state_indices", {b}),
+            indices(len, "context_lengths", {b}), indices(parents, "parent_ids", {b, T}),
+            update, fit32(b, "batch"), active, fit32(T, "T"), xd, bd,
+            dense<int32_t>(err, "err_flags", {1}, ScalarType::Int),
+            stream_of(stream, r.device));
     });
 }
 
@@ -342,12 +355,14 @@ PyObject *conv_replay(PyObject *, PyObject *const *args, Py_ssize_t n)
         const int64_t ld = tokens(xbc, "xbc", {b, T, ch}, 2);
         const ConvPool cp = conv_pool(pool, xbc, ch, width, cs, cc, ck, P);
         const c10::cuda::CUDAGuard on((c10::DeviceIndex)r.device);
-        return fn(xbc.data_ptr(), code(xbc, "xbc"), ld, cp.p, cp.slot, cp.c, cp.k, width, cp.P,
-                  indices(&acc, "accepted_lengths", {b}), indices(idx, "state_indices", {b}),
-                  fit32(b, "batch"), active, fit32(T, "T"), fit32(ch, "channels"),
-                  node_lists(ids, "accepted_node_ids", b, most, acc), fit32(most, "maxAcceptLen"),
-                  dense<int32_t>(err, "err_flags", {1}, ScalarType::Int),
-                  stream_of(stream, r.device));
+        return unlocked(
+            fn, xbc.data_ptr(), code(xbc, "xbc"), ld, cp.p, cp.slot, cp.c, cp.k, width,
+            cp.P,
+            indices(&acc, "accepted_lengths", {b}), indices(idx, "state_indices", {b}),
+            fit32(b, "batch"), active, fit32(T, "T"), fit32(ch, "channels"),
+            node_lists(ids, "accepted_node_ids", b, most, acc), fit32(most, "maxAcceptLen"),
+            dense<int32_t>(err, "err_flags", {1}, ScalarType::Int),
+            stream_of(stream, r.device));
     });
 }
 
@@ -438,16 +453,18 @@ PyObject *scan_prefill_(PyObject *, PyObject *const *args, Py_ssize_t n)
         const Tensor *const len = r.optional("context_lengths");
         const int update = r.truth();
         const c10::cuda::CUDAGuard on((c10::DeviceIndex)r.device);
-        return fn(s.x->data_ptr(), code(*s.x, "x"), s.ldx, s.dt->data_ptr(), code(*s.dt, "dt"), s.lddt,
-                  dense<const float>(s.A, "A", {s.ch, s.N}, ScalarType::Float), s.B->data_ptr(),
-                  Scan::ptr(s.C), code(*s.B, "B"), s.ldb, s.ldc, s.f32(s.bias, "dt_bias"),
-                  s.f32(s.D, "D"), Scan::ptr(s.z), s.ldz, s.state->data_ptr(),
-                  code(*s.state, "state"), s.stride, s.P, Scan::ptr(s.out),
-                  indices(s.idx, "state_indices", {s.b}), indices(len, "context_lengths", {s.b}),
-                  update, fit32(s.b, "batch"), s.active, fit32(s.T, "T"), fit32(s.ch, "channels"),
-                  fit32(s.G, "groups"), fit32(s.N, "dstate"), s.softplus,
-                  dense<int32_t>(s.err, "err_flags", {1}, ScalarType::Int),
-                  stream_of(stream, r.device));
+        return unlocked(
+            fn, s.x->data_ptr(), code(*s.x, "x"), s.ldx, s.dt->data_ptr(),
+            code(*s.dt, "dt"), s.lddt,
+            dense<const float>(s.A, "A", {s.ch, s.N}, ScalarType::Float), s.B->data_ptr(),
+            Scan::ptr(s.C), code(*s.B, "B"), s.ldb, s.ldc, s.f32(s.bias, "dt_bias"),
+            s.f32(s.D, "D"), Scan::ptr(s.z), s.ldz, s.state->data_ptr(),
+            code(*s.state, "state"), s.stride, s.P, Scan::ptr(s.out),
+            indices(s.idx, "state_indices", {s.b}), indices(len, "context_lengths", {s.b}),
+            update, fit32(s.b, "batch"), s.active, fit32(s.T, "T"), fit32(s.ch, "channels"),
+            fit32(s.G, "groups"), fit32(s.N, "dstate"), s.softplus,
+            dense<int32_t>(s.err, "err_flags", {1}, ScalarType::Int),
+            stream_of(stream, r.device));
     });
 }
 
@@ -456,15 +473,17 @@ PyObject *scan_decode_(PyObject *, PyObject *const *args, Py_ssize_t n)
     return guarded<decltype(&scan_decode)>(args, n, [](Reader &r, auto fn, PyObject *stream) {
         const Scan s(r, 1);
         const c10::cuda::CUDAGuard on((c10::DeviceIndex)r.device);
-        return fn(s.x->data_ptr(), code(*s.x, "x"), s.ldx, s.dt->data_ptr(), code(*s.dt, "dt"), s.lddt,
-                  dense<const float>(s.A, "A", {s.ch, s.N}, ScalarType::Float), s.B->data_ptr(),
-                  Scan::ptr(s.C), code(*s.B, "B"), s.ldb, s.ldc, s.f32(s.bias, "dt_bias"),
-                  s.f32(s.D, "D"), Scan::ptr(s.z), s.ldz, s.state->data_ptr(),
-                  code(*s.state, "state"), s.stride, s.P, Scan::ptr(s.out),
-                  indices(s.idx, "state_indices", {s.b}), fit32(s.b, "batch"), s.active,
-                  fit32(s.ch, "channels"), fit32(s.G, "groups"), fit32(s.N, "dstate"), s.softplus,
-                  dense<int32_t>(s.err, "err_flags", {1}, ScalarType::Int),
-                  stream_of(stream, r.device));
+        return unlocked(
+            fn, s.x->data_ptr(), code(*s.x, "x"), s.ldx, s.dt->data_ptr(),
+            code(*s.dt, "dt"), s.lddt,
+            dense<const float>(s.A, "A", {s.ch, s.N}, ScalarType::Float), s.B->data_ptr(),
+            Scan::ptr(s.C), code(*s.B, "B"), s.ldb, s.ldc, s.f32(s.bias, "dt_bias"),
+            s.f32(s.D, "D"), Scan::ptr(s.z), s.ldz, s.state->data_ptr(),
+            code(*s.state, "state"), s.stride, s.P, Scan::ptr(s.out),
+            indices(s.idx, "state_indices", {s.b}), fit32(s.b, "batch"), s.active,
+            fit32(s.ch, "channels"), fit32(s.G, "groups"), fit32(s.N, "dstate"), s.softplus,
+            dense<int32_t>(s.err, "err_flags", {1}, ScalarType::Int),
+            stream_of(stream, r.device));
     });
 }
 
@@ -492,18 +511,19 @@ PyObject *spec_verify_(PyObject *, PyObject *const *args, Py_ssize_t n)
         const int64_t ldp = tokens(p, "target_probs", {b, T, V}, 2);
         const int64_t ldq = q ? tokens(*q, "draft_probs", {b, T > 0 ? T - 1 : 0, V}, 2) : 0;
         const c10::cuda::CUDAGuard on((c10::DeviceIndex)r.device);
-        return fn(indices(&tok, "tokens", {b, T}), p.data_ptr(), q ? q->data_ptr() : nullptr,
-                  code(p, "target_probs"), ldp, ldq,
-                  dense<const float>(&u, "uniforms", {b, T}, ScalarType::Float),
-                  dense<const float>(&us, "uniform_sample", {b}, ScalarType::Float),
-                  indices(len, "context_lengths", {b}), indices(parents, "parent_ids", {b, T}),
-                  indices(idx, "state_indices", {b}),
-                  dense<int32_t>(&acc, "accepted_lengths", {b}, ScalarType::Int),
-                  dense<int32_t>(&nxt, "next_tokens", {b}, ScalarType::Int),
-                  node_lists(nodes, "accepted_node_ids", b, most, acc),
-                  fit32(most, "maxAcceptLen"), fit32(b, "batch"), active, fit32(T, "T"),
-                  fit32(V, "vocab"), dense<int32_t>(err, "err_flags", {1}, ScalarType::Int),
-                  stream_of(stream, r.device));
+        return unlocked(
+            fn, indices(&tok, "tokens", {b, T}), p.data_ptr(),
+            q ? q->data_ptr() : nullptr, code(p, "target_probs"), ldp, ldq,
+            dense<const float>(&u, "uniforms", {b, T}, ScalarType::Float),
+            dense<const float>(&us, "uniform_sample", {b}, ScalarType::Float),
+            indices(len, "context_lengths", {b}), indices(parents, "parent_ids", {b, T}),
+            indices(idx, "state_indices", {b}),
+            dense<int32_t>(&acc, "accepted_lengths", {b}, ScalarType::Int),
+            dense<int32_t>(&nxt, "next_tokens", {b}, ScalarType::Int),
+            node_lists(nodes, "accepted_node_ids", b, most, acc),
+            fit32(most, "maxAcceptLen"), fit32(b, "batch"), active, fit32(T, "T"),
+            fit32(V, "vocab"), dense<int32_t>(err, "err_flags", {1}, ScalarType::Int),
+            stream_of(stream, r.device));
     });
 }
 

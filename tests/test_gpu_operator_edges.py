@@ -1,5 +1,7 @@
 """GPU tests of the calls at the edges of the convolution, scan and verification operators."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -47,3 +49,31 @@ def test_a_replay_of_an_empty_list_of_nodes_takes_nothing():
         else:
             ssu.ssu_replay(got, stash, acc, accepted_node_ids=none, err_flags=err)
         assert same_bits(got, pool) and int(err.item()) == ssu.FLAG_ACCEPTED_RANGE
+
+
+# ---------------------------------------------------------------- the binding
+
+def test_launches_run_without_the_interpreter_lock():
+    """A launch into a full queue waits for the device: the marshalled entry points are called
+    as ctypes calls them, with the lock released (in place of the entry point here: the
+    interpreter's own question whether this thread holds it)."""
+    held = ctypes.cast(ctypes.pythonapi.PyGILState_Check, ctypes.c_void_p).value
+    assert ctypes.pythonapi.PyGILState_Check() == 1
+    native = ssu._load_marshal()
+    x, B = torch.zeros(2, 3, 8, **DEV), torch.zeros(2, 3, 1, 8, **DEV)
+    pool, w = torch.zeros(2, 8, 8, **DEV), torch.zeros(8, 2, **DEV)
+    A, i = torch.zeros(8, 8, **DEV), torch.zeros(2, dtype=I32, **DEV)
+    p, tok = torch.zeros(2, 3, 9, **DEV), torch.zeros(2, 3, dtype=I32, **DEV)
+    no = None
+    calls = {
+        "ssu_conv_prefill": (x, w, torch.zeros(2, 8, 1, **DEV), x, no, no, no, no, no, no, no,
+                             2, 8, 1, 1, True, True, no, no),
+        "ssu_conv_replay": (x, torch.zeros(2, 8, 1, **DEV), i, no, no, no, 2, 8, 1, 1, no, no),
+        "scan_prefill": (x, x, A, B, B, pool, x, no, no, no, no, no, True, no, no, no, no, True),
+        "scan_decode": (x[:, 0], x[:, 0], A, B[:, 0], B[:, 0], pool, x[:, 0].clone(), no,
+                        no, no, no, no, True, no, no, no),
+        "spec_verify": (tok, p, torch.zeros(2, 3, **DEV), torch.zeros(2, **DEV), i, i, no, no, no,
+                        no, no, no, no),
+    }
+    for name, args in calls.items():
+        assert getattr(native, name)(held, None, *args) == 0, name
