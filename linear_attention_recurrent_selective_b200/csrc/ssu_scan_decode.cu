@@ -175,7 +175,9 @@ scan_decode_kernel(const __grid_constant__ ScanArgs a, const int blocks)
         const bool second = i & 1;
         float v = 0.f;                              // padding row: zero
         if (sl >= 0) {
-            v = fmaf(skip, second ? x[i / 2].y : x[i / 2].x, second ? o[i / 2].y : o[i / 2].x);
+            v = second ? o[i / 2].y : o[i / 2].x;
+            if (a.Dp)                               // (0 times an infinite x would be a NaN)
+                v = fmaf(skip, second ? x[i / 2].y : x[i / 2].x, v);
             if (a.z)
                 v *= gate2(both(second ? z[i / 2].y : z[i / 2].x), xt).x;
         }

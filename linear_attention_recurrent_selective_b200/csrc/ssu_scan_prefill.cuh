@@ -264,7 +264,7 @@ __device__ __forceinline__ void run_tokens(const ScanArgs &a, Lane<CH> &st, uint
     const int xt = DT < 0 ? a.x_dtype : DT, dtt = DT < 0 ? a.dt_dtype : DT;
     const int bct = DT < 0 ? a.bc_dtype : DT;
     const int ex = esize(xt), ed = esize(dtt), eb = esize(bct);
-    const bool gated = kOut && a.z, softplus = a.softplus;
+    const bool gated = kOut && a.z, skips = kOut && a.Dp, softplus = a.softplus;
     const Raw lay = raw_layout<N, CH, TM>(ex, ed, eb, a.z);
     uint8_t *const raw0 = smem + T::kFixed;
     const char *const gx = static_cast<const char *>(a.x) + (row * a.ldx + blk.d0) * ex;
@@ -282,7 +282,8 @@ __device__ __forceinline__ void run_tokens(const ScanArgs &a, Lane<CH> &st, uint
         bias.x = live ? a.dt_bias[d] : 0.f;
         bias.y = CH == 1 ? bias.x : live1 ? a.dt_bias[d + 1] : 0.f;
     }
-    if (kOut && a.Dp) {
+    const uint32_t keep = skips ? ~0u : 0u;
+    if (skips) {
         skip.x = live ? a.Dp[d] : 0.f;
         skip.y = CH == 1 ? skip.x : live1 ? a.Dp[d + 1] : 0.f;
     }
@@ -340,6 +341,9 @@ __device__ __forceinline__ void run_tokens(const ScanArgs &a, Lane<CH> &st, uint
                 dt[p].x = t0 + ta < t_end ? dt[p].x : 0.f;
                 dt[p].y = t0 + tb < t_end ? dt[p].y : 0.f;
                 dx[p] = mul2(dt[p], x[p]);
+                // for D x; without D 0, which an infinite x times a zero D would not be
+                x[p].x = __uint_as_float(__float_as_uint(x[p].x) & keep);
+                x[p].y = __uint_as_float(__float_as_uint(x[p].y) & keep);
             }
         };
         float2 x[kPr], dt[kPr], dx[kPr];

@@ -5,12 +5,13 @@ import ctypes
 import pytest
 import torch
 
+import test_gpu_scan as ts
 from linear_attention_recurrent_selective_b200 import ssu
 from parity import same_bits
 
 pytestmark = pytest.mark.gpu
 
-I32 = torch.int32
+F32, I32 = torch.float32, torch.int32
 DEV = dict(device="cuda")
 
 
@@ -49,6 +50,29 @@ def test_a_replay_of_an_empty_list_of_nodes_takes_nothing():
         else:
             ssu.ssu_replay(got, stash, acc, accepted_node_ids=none, err_flags=err)
         assert same_bits(got, pool) and int(err.item()) == ssu.FLAG_ACCEPTED_RANGE
+
+
+# ---------------------------------------------------------------- inputs that overflow
+
+@pytest.mark.parametrize("T,ch,N,batch", [(9, 40, 16, 2), (300, 16, 16, 2), (1100, 16, 64, 1),
+                                          (9, 285, 64, 40)])
+def test_an_infinite_input_without_a_skip_connection(T, ch, N, batch):
+    """Without D the output is the sum of states alone: all of one sign, it is infinite."""
+    c = ts.make(T, batch, T, ch, 1, N, F32, z=False, D=False, bias=False, positive=True)
+    for k in ("B", "C", "x"):
+        c[k] = (c[k][0].abs() + 0.1, c[k][1])
+    c["dt"] = (c["dt"][0] + 0.01, c["dt"][1])
+    c["A"], c["pool"] = c["A"] * 1e-3, c["pool"].abs()
+    at = T // 2
+    c["x"][0][:, at, ::3] = float("inf")
+    o, pool, _ = ts.run(c, softplus=False)
+    want = torch.zeros(T, ch, dtype=torch.bool)
+    want[at:, ::3] = True
+    assert torch.equal(o == float("inf"), want.expand(batch, T, ch))
+    assert not torch.isnan(o).any() and not torch.isnan(pool).any()
+    c["x"] = (c["x"][0][:, at:], c["x"][1])
+    o, _, _ = ts.run_decode(c, softplus=False)
+    assert torch.equal(o == float("inf"), want[at].expand(batch, ch)) and not torch.isnan(o).any()
 
 
 # ---------------------------------------------------------------- the binding
