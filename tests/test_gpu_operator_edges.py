@@ -5,13 +5,15 @@ import ctypes
 import pytest
 import torch
 
+import plain_ops as po
 import test_gpu_scan as ts
 from linear_attention_recurrent_selective_b200 import ssu
 from parity import same_bits
 
 pytestmark = pytest.mark.gpu
 
-F32, I32 = torch.float32, torch.int32
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+I32 = torch.int32
 DEV = dict(device="cuda")
 
 
@@ -73,6 +75,54 @@ def test_an_infinite_input_without_a_skip_connection(T, ch, N, batch):
     c["x"] = (c["x"][0][:, at:], c["x"][1])
     o, _, _ = ts.run_decode(c, softplus=False)
     assert torch.equal(o == float("inf"), want[at].expand(batch, ch)) and not torch.isnan(o).any()
+
+
+# ---------------------------------------------------------------- gates far below zero
+
+def silu_bound(v, dtype):
+    """v sigmoid(v) in 64 bits and how far the kernels may be off: a few fp32 steps and those of
+    the exponential's rounded argument, and the output's rounding. The arithmetic of 16-bit
+    outputs has no 1 / (1 + e^-v) below 2^-126, where v is beyond -88 and the result 2^-119."""
+    v = v.double()
+    want = v * torch.sigmoid(v)
+    lim = want.abs() * (8 + 2 * v.abs()) * po.U
+    lim = lim + (want.abs() + lim) * po.half_step(dtype) + po.tiny(dtype)
+    return want, lim + (0.0 if dtype == F32 else 2.0 ** -119)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("T", [1, 5, 32])
+def test_silu_over_its_whole_range(dtype, T):
+    """From gates of -110, whose outputs are below the smallest normal number, to 110, and of
+    every size around zero."""
+    ch = 64
+    v = torch.cat([torch.linspace(-110, 110, T * ch // 2),
+                   torch.logspace(-36, 2, T * ch - T * ch // 2) * -1.0]).view(1, T, ch).to(dtype)
+    w = torch.tensor([0.0, 1.0]).expand(ch, 2).to(dtype).contiguous()
+    x = torch.empty(1, T, ch, dtype=dtype, **DEV)
+    ssu.ssu_conv_prefill(v.cuda(), w.cuda(), torch.zeros(1, ch, 1, dtype=dtype, **DEV), x, width=2,
+                         conv_strides=(ch, 1, 1))
+    want, lim = silu_bound(v, dtype)
+    bad = (x.cpu().double() - want).abs() > lim
+    assert not bad.any(), (v[bad][:4].tolist(), x.cpu()[bad][:4].tolist(), want[bad][:4].tolist())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_scan_gates_over_their_whole_range(dtype):
+    """A state and inputs of zero but for x, and D = 1: the output is x silu(z)."""
+    T, ch, N = 8, 64, 16
+    z = torch.linspace(-110, 110, T * ch).view(1, T, ch).to(dtype).cuda()
+    one, none = torch.ones_like(z), torch.zeros(1, T, 1, N, dtype=dtype, **DEV)
+    A, D = -torch.ones(ch, N, **DEV), torch.ones(ch, **DEV)
+    want, lim = silu_bound(z.cpu(), dtype)
+    out = torch.empty_like(z)
+    ssu.scan_prefill(one, one, A, none, none, torch.zeros(1, ch, N, **DEV), out, D=D, z=z)
+    assert ((out.cpu().double() - want).abs() <= lim).all()
+    for t in range(T):
+        y = torch.empty(1, ch, dtype=dtype, **DEV)
+        ssu.scan_decode(one[:, t], one[:, t], A, none[:, t], none[:, t],
+                        torch.zeros(1, ch, N, **DEV), y, D=D, z=z[:, t])
+        assert ((y.cpu().double() - want[:, t]).abs() <= lim[:, t]).all()
 
 
 # ---------------------------------------------------------------- the binding
