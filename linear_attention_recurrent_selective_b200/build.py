@@ -5,7 +5,9 @@ Objects go to _build/ at the repository root; the shared library lands next to t
 file so that it travels with the package.
 
 The Python binding's native argument marshalling (csrc/marshal.cpp, a CPython module that
-reads torch tensors) is built beside it as _marshal.so with the C++ compiler.
+reads torch tensors) is built beside it as _marshal.so with the C++ compiler. The library does
+not need it: where it cannot be built (no C++ compiler, a torch without CUDA) the library is
+built all the same, with a warning.
 
 The same sources also build libssu_waittest.so (objects in _build/waittest/), with
 SSU_WAIT_TEST defined: the test suite's library in which a chosen bounded wait can be
@@ -22,6 +24,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -85,13 +88,20 @@ def build_marshal(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, waittest: bool = False) -> str:
-    """Build libssu.so and _marshal.so (or, with waittest, the test library
-    libssu_waittest.so)."""
+    """Build libssu.so and, where that can be done, _marshal.so (or, with waittest, the test
+    library libssu_waittest.so)."""
     lib = WAITTEST_LIB if waittest else LIB
+    if force or not up_to_date(lib):
+        _build_library(lib, verbose, waittest)
     if not waittest:
-        build_marshal(force)
-    if not force and up_to_date(lib):
-        return lib
+        try:
+            build_marshal(force)
+        except (ImportError, OSError, RuntimeError) as e:
+            warnings.warn(f"libssu.so is built, the binding's _marshal.so is not: {e}", stacklevel=2)
+    return lib
+
+
+def _build_library(lib: str, verbose: bool, waittest: bool) -> None:
     objdir = os.path.join(BUILD, "waittest") if waittest else BUILD
     os.makedirs(objdir, exist_ok=True)
     cc = nvcc()
@@ -117,7 +127,6 @@ def build(force: bool = False, verbose: bool = False, waittest: bool = False) ->
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
-    return lib
 
 
 if __name__ == "__main__":
