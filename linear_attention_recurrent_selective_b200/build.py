@@ -5,9 +5,10 @@ Objects go to _build/ at the repository root; the shared library lands next to t
 file so that it travels with the package.
 
 The Python binding's native argument marshalling (csrc/marshal.cpp, a CPython module that
-reads torch tensors) is built beside it as _marshal.so with the C++ compiler. The library does
-not need it: where it cannot be built (no C++ compiler, a torch without CUDA) the library is
-built all the same, with a warning.
+reads torch tensors) is built beside it with the C++ compiler, under a name that says which
+torch and which Python it was built against (_marshal.<torch>.<python>.so): it reads their
+objects, and is of no use to others. The library does not need it: where it cannot be built
+(no C++ compiler, a torch without CUDA) the library is built all the same, with a warning.
 
 The same sources also build libssu_waittest.so (objects in _build/waittest/), with
 SSU_WAIT_TEST defined: the test suite's library in which a chosen bounded wait can be
@@ -32,7 +33,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libssu.so")
-MARSHAL = os.path.join(PKG, "_marshal.so")
 WAITTEST_LIB = os.path.join(PKG, "libssu_waittest.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -63,18 +63,25 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps() + [__file__])
 
 
-def build_marshal(force: bool = False) -> str:
-    """Build _marshal.so, the binding's native argument marshalling."""
-    src = os.path.join(CSRC, "marshal.cpp")
-    deps = [src, __file__] + glob.glob(os.path.join(INCLUDE, "*.h"))
-    if not force and os.path.exists(MARSHAL) and \
-            all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in deps):
-        return MARSHAL
+def marshal_path() -> str:
+    """Where the binding's native module for this torch and this Python is."""
     import torch
+    tag = sysconfig.get_config_var("EXT_SUFFIX")
+    return os.path.join(PKG, f"_marshal.{torch.__version__}{tag}")
+
+
+def build_marshal(force: bool = False) -> str:
+    """Build the binding's native argument marshalling."""
+    import torch
+    src, out = os.path.join(CSRC, "marshal.cpp"), marshal_path()
+    deps = [src, __file__] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(out) and \
+            all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps):
+        return out
     home = os.path.dirname(torch.__file__)
     inc, libs = os.path.join(home, "include"), os.path.join(home, "lib")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
-    tmp = MARSHAL + ".tmp"
+    tmp = out + ".tmp"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
            "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
@@ -83,13 +90,13 @@ def build_marshal(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, MARSHAL)
-    return MARSHAL
+    os.replace(tmp, out)
+    return out
 
 
 def build(force: bool = False, verbose: bool = False, waittest: bool = False) -> str:
-    """Build libssu.so and, where that can be done, _marshal.so (or, with waittest, the test
-    library libssu_waittest.so)."""
+    """Build libssu.so and, where that can be done, the binding's native module (or, with
+    waittest, the test library libssu_waittest.so)."""
     lib = WAITTEST_LIB if waittest else LIB
     if force or not up_to_date(lib):
         _build_library(lib, verbose, waittest)
@@ -97,7 +104,8 @@ def build(force: bool = False, verbose: bool = False, waittest: bool = False) ->
         try:
             build_marshal(force)
         except (ImportError, OSError, RuntimeError) as e:
-            warnings.warn(f"libssu.so is built, the binding's _marshal.so is not: {e}", stacklevel=2)
+            warnings.warn(f"libssu.so is built, the binding's native module is not: {e}",
+                          stacklevel=2)
     return lib
 
 

@@ -32,6 +32,7 @@ Semantics (Selective State Update page of the TensorRT-Edge-LLM C++ API):
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional
 
@@ -381,13 +382,18 @@ def _call(name, stream, *args):
 
 
 def _load_marshal():
+    """The native module that was built for this torch and this Python."""
+    from .build import marshal_path
+    path = marshal_path()
+    spec = importlib.util.spec_from_file_location(f"{__package__}._marshal", path)
     try:
-        from . import _marshal
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
     except ImportError as e:
         raise SSULibraryMissing(
-            f"the binding's _marshal.so is missing or does not load ({e}): build it with "
+            f"the binding's {path} is missing or does not load ({e}): build it with "
             "`python -m linear_attention_recurrent_selective_b200.build`") from e
-    return _marshal
+    return module
 
 
 def _debug_slots(state_indices, pool, P, active, stream):
