@@ -151,3 +151,58 @@ def test_launches_run_without_the_interpreter_lock():
     }
     for name, args in calls.items():
         assert getattr(native, name)(held, None, *args) == 0, name
+
+
+# ---------------------------------------------------------------- forms of large calls
+
+@pytest.mark.parametrize("ch,G", [(285, 3), (288, 3), (301, 1)])
+@pytest.mark.parametrize("N,xdt", [(64, BF16), (128, F32), (256, F16)])
+def test_many_rows_of_many_states(N, ch, G, xdt):
+    """64 states and more with rows enough for two channels a lane: odd channels, groups and
+    more ragged rows than are ordered by length, padding and empty rows among them."""
+    b, T = 40, 19
+    order = torch.randperm(b + 2, generator=po.generator(N))[:b].tolist()
+    order[5], order[17] = -1, b + 2
+    c = ts.make(N + ch, b, T, ch, G, N, xdt, slots=order)
+    lengths = torch.randint(0, T + 1, (b,), generator=po.generator(ch)).to(I32)
+    lengths[:3] = torch.tensor([0, T, 1])
+    ts.check(c, lengths)
+    ts.check(c, lengths, out=False)
+
+
+def test_more_ragged_rows_than_are_ordered():
+    c = ts.make(33, 40, 35, 24, 1, 16, BF16)
+    ts.check(c, torch.randint(0, 36, (40,), generator=po.generator(2)).to(I32))
+
+
+@pytest.mark.parametrize("N", [128, 256])
+@pytest.mark.parametrize("ch,G", [(1, 1), (34, 2)])
+def test_one_long_row_of_many_states(N, ch, G):
+    """One row over as many CTAs as a cluster holds."""
+    c = ts.make(N + ch, 1, 3000, ch, G, N, BF16)
+    c["A"] = c["A"] * 0.05
+    ts.check(c)
+    ts.check(c, torch.tensor([2049], dtype=I32), out=False)
+
+
+# ---------------------------------------------------------------- slots past 32 bits
+
+def test_single_tokens_of_slots_past_32_bits():
+    """Outputs and states of one token whose slot lies beyond 2^31 elements of the pool."""
+    ch, N, P = 5120, 16, 27000
+    assert (P - 1) * ch * N > 2 ** 31
+    c = ts.make(15, 2, 1, ch, 1, N, BF16, sdt=BF16)
+    small = c["pool"].view(c["P"], ch, N)
+    slots, far = [int(s) for s in c["slots"]], [P - 1, 7]
+    pool = torch.zeros(P, ch, N, dtype=BF16, **DEV)
+    for f, s in zip(far, slots):
+        pool[f] = small[s].cuda()
+    want, state, lim, slim, _ = ts.plain_decode(c)
+    one = lambda k: ts.cut(c[k], 1)[:, 0].contiguous()  # noqa: E731
+    out = torch.empty(2, ch, dtype=BF16, **DEV)
+    ssu.scan_decode(one("x"), one("dt"), c["A"].cuda(), one("B"), one("C"), pool, out,
+                    D=c["D"].cuda(), z=one("z"), dt_bias=c["bias"].cuda(),
+                    state_indices=torch.tensor(far, dtype=I32, **DEV))
+    ts.near(out.cpu(), want, lim, BF16, "out")
+    ts.near(pool[far].cpu(), state[slots], slim[slots], BF16, "state")
+    assert int((pool != 0).flatten(1).any(1).sum()) == 2
