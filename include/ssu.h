@@ -272,7 +272,7 @@ int ssu_conv_decode(const void *xbc, int x_dtype, const void *conv_weight,
  *                update_state == 0): the inputs before node t are its ancestors (parent, grandparent, ...), then
  *                the window. A node with a parent outside [-1, L_b) among its width-1
  *                nearest ancestors gets outputs 0 and SSU_FLAG_TREE.
- *   width 1..16; batch, T and the channels together up to 2^30. Padding rows write zeros to
+ *   width 1..16; batch, T and x_dim + 2*bc_dim up to 2^30 each. Padding rows write zeros to
  *   the outputs at every t < T.
  * xbc must not overlap the outputs. One launch.
  */
@@ -380,8 +380,8 @@ int scan_decode(const void *x, int x_dtype, int64_t x_stride, const void *dt, in
  *                    for L_b == 0 and for a tree without a root)
  *   accepted_node_ids [batch, max_accept_len] int32 (optional, trees only): the path, -1
  *                    beyond it
- * Nothing is written when T == 0 (the Python binding refuses it). The outputs overlap no
- * input.
+ * T and vocab up to 2^30. Nothing is written when T == 0 (the Python binding refuses it). The
+ * outputs overlap no input.
  * Flags: SSU_FLAG_TOKEN (a drafted token outside [0, vocab), never accepted), SSU_FLAG_TREE
  * (a parent outside [-1, L_b), or no root: the node is never accepted), SSU_FLAG_NO_MASS
  * (p itself holds no mass: next token -1), and the length flags. One launch.

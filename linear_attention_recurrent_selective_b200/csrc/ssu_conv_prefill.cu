@@ -13,12 +13,15 @@
 // W + 3 multiply-adds and two special-function operations (the sigmoid); windows are
 // touched once per row.
 //
-// Measured (B200, bfloat16, 5376 channels, width 4): 16 ragged rows of up to 512 tokens 26.0
-// us, 16 full ones 39 us (0.71 of the copy rate; a full wave's strips end together, and the
-// sigmoid's two special-function operations an element take half of that time); one token of
-// each of 256 rows 5.6 us (0.61); draft trees of 16 x 128 nodes in half precision 18.5 us
-// (0.37: a CTA loads, walks, computes and stores one after the other, in little over one
-// wave); the commit of 64 rows 3.1 us, of which a launch alone is about 2.5.
+// Measured (B200, bfloat16, 5376 channels, width 4; the inputs of a call not in L2): 16 ragged
+// rows of up to 512 tokens 24 to 28 us by their lengths, 16 full ones 38.5 us (0.71 of the copy
+// rate; DRAM 40 %, the special-function unit 58 % and issue slots 45 % busy: 16 warps an SM,
+// whose strips end in waves); one token of each of 256 rows 8.7 us (0.39; 5.7 where the windows
+// are in L2); 64 rows of 5 drafted tokens 7.8 us; draft trees of 16 x 128 nodes in half
+// precision 18.5 us (0.37: a CTA loads, walks, computes and stores one after the other, in
+// little over one wave); the commit of 64 rows 4.5 us (3.1 in L2), of which a launch alone is
+// about 2.5. The full rows again: in fp32 62 us (0.89), at width 5 52 us, at 8 76 us, at 16
+// 816 us (tap by tap), with channels that are not on 16 bytes 80 us.
 //
 // Layout: a thread owns VEC neighbouring channels (one access of a row; one channel where
 // rows or segments are not aligned) over a strip of up to kStrip tokens, and slides the
@@ -438,7 +441,7 @@ conv_prefill_kernel(const __grid_constant__ ConvPrefillArgs a, const int groups,
 }
 
 // The same for whole 16-byte vectors and long rows: each thread streams its vectors of the
-// strip through a ring of its own in shared memory by cp.async, kStages groups of kGroup
+// strip through a ring of its own in shared memory by cp.async, kStages - 1 groups of kGroup
 // tokens ahead, so that what is in flight does not take registers (a register prefetch of
 // one group kept 14 KB an SM in flight: 60 us for 16 rows of 512 tokens of 5376 channels in
 // bfloat16, against 39 us this way, DRAM 38 % busy). Only its own copies are waited for: no barrier.

@@ -34,7 +34,7 @@ __device__ __forceinline__ float2 decay2(float2 s, float2 r)
 __device__ __forceinline__ float2 softplus2(float2 v)
 {
     const float kLog2e = 1.44269504f, kLog2eLo = 1.92596e-8f, kLn2 = 0.693147181f;
-    const float2 a = make_float2(fmaxf(-fabsf(v.x), -104.f),       // e^-104 is 0 in fp32
+    const float2 a = make_float2(fmaxf(-fabsf(v.x), -104.f),       // 0 from e^-87.3 on
                                  fmaxf(-fabsf(v.y), -104.f));
     const float2 hi = mul2(a, both(kLog2e));
     const float2 lo = fma2(a, both(kLog2eLo), fma2(a, both(kLog2e), make_float2(-hi.x, -hi.y)));

@@ -8,7 +8,7 @@
 // exponential and four multiply-adds per state; x, dt, z and out are 1/N of it each.
 //
 // Measured (B200, 256 rows of 5120 channels, 16 states, fp32 pool, bfloat16 inputs): 33.3 us,
-// 0.82 of the copy rate; issue slots are 79 % busy, the conversions of B and C and the
+// 0.83 of the copy rate; issue slots are 79 % busy, the conversions of B and C and the
 // exchange between lanes ahead of the recurrence itself. Loading each operand where it is
 // used, element by element, took 71 us.
 //

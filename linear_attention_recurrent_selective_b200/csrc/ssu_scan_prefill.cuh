@@ -9,9 +9,12 @@
 // Bound: the special-function unit (16 exponentials a clock and SM, so one clock per
 // (token, channel) and SM at N = 16), ahead of memory (x, dt, z, out: 8 bytes).
 //
-// Measured (B200, bfloat16, 5120 channels, 16 states): 16 full rows of 512 tokens 263 us, 16
-// ragged ones 146 us, against 88 us (full: 174) for the special-function operations alone
-// (16 decays, 1 for the softplus, 2 for the gate); that unit is 69 % busy and issue slots 65 %.
+// Measured (B200, bfloat16, 5120 channels, 16 states): 16 full rows of 512 tokens 265 us, 16
+// ragged ones 126 to 155 us by their lengths, against 88 us (full: 174) for the special-function
+// operations alone (16 decays, 1 for the softplus, 2 for the gate); that unit is 69 % busy and
+// issue slots 65 %. The ragged rows with 8 states 110 us, with 32 250 us; of 2048 channels with
+// 64 states 214 us, with 128 337 us. 64 rows of 5 drafted tokens 73 us: a chunk's groups behind
+// the row's end are run as well.
 // Without the decays' exponentials the full rows take 253 of then 286 us, without softplus
 // and gate 233, without the exchanges between lanes 251, and B and C cost nothing: what
 // bounds it is the sum of what a warp issues. One row of 4099 tokens of 1000 channels: 79 us
@@ -49,7 +52,13 @@ namespace cg = cooperative_groups;
 
 constexpr int kStates = 8;            // of a lane
 constexpr int kMinWarps = 16;         // of an SM: at most 128 registers a thread
-constexpr int kFill = 2700;           // warps of a full card (148 SMs of 18)
+// Most warps that cutting rows into segments may make, a little above the 2368 that the card
+// holds at a time (148 SMs of kMinWarps). A row of 4096 tokens of 5120 channels takes 353 us in
+// 2560 warps and 422 in half as many, one of 2560 channels 186 and 210. Twice the warps lose:
+// 4099 tokens of 1000 channels 164 us in 4096 against 79, two rows of 2048 tokens of 2048
+// channels 135 against 131, four of 5120 channels 541 cut into 5120 warps against 369 uncut
+// (but the one row of 5120 channels 322 against 353).
+constexpr int kFill = 2700;
 constexpr int kMaxParts = 16;         // CTAs of a cluster (above 8 by opt-in)
 
 // CH: neighbouring channels of a lane, 1 or 2. TM: teams of a CTA, each with a segment of the
@@ -510,7 +519,8 @@ scan_prefill_kernel(const __grid_constant__ ScanArgs a, const int blocks, const 
         }
     };
     // the state behind a segment that ends in `end`: `first` replaces it, others let it decay
-    // over their steps and add what they end in from zero
+    // over their steps and add what they end in from zero (one exponential a segment: its mean
+    // error, which the decays of single tokens are corrected for, does not gather)
     const auto fold = [&](const float *end, bool replace) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {

@@ -18,12 +18,12 @@
 // Bound: memory for many rows (one row of p and at most one of q per sequence), latency
 // for one: a few dependent loads find the row, then it is streamed once.
 //
-// Measured (B200): 64 sequences of 4 drafted tokens over 2^17 tokens in fp32 18.9 us, of which
-// the rows' sums are 12.5 (0.79 of the copy rate), finding the row and the clusters' meeting
-// 4.7 (6.2 where a length or an index was waited for before the tokens) and the drawn token
-// 1.7; one sequence over 65537 tokens in bfloat16 7.2 us; 16 trees of 128 nodes over 32768
-// tokens 10.3 us. Sums as pairs of floats instead of doubles: 33.7 us
-// against 27.3 for the same loop.
+// Measured (B200, where the distributions are not in L2): 64 sequences of 4 drafted tokens over
+// 2^17 tokens in fp32 19.1 us, of which the rows' sums are 12.5 (0.79 of the copy rate), finding
+// the row and the clusters' meeting 4.7 (6.2 where a length or an index was waited for before
+// the tokens) and the drawn token 1.7; over 151936 tokens 23.0 us, over 50001, where p and q
+// start at different offsets from 16 bytes, 13.9 us; one sequence over 65537 tokens in bfloat16
+// 7.8 us; 16 trees of 128 nodes over 32768 tokens 11.5 us. Sums as pairs of floats instead of doubles: 33.7 us against 27.3 for the same loop.
 //
 // Layout: a cluster of CTAs per sequence. Every CTA walks the chain or tree itself (a few
 // gathers), then each warp sums one contiguous region of the row in kChunks chunks, whose
