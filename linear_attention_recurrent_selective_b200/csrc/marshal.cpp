@@ -250,12 +250,15 @@ ssu_stream_t stream_of(PyObject *stream, int device)
 
 // Calls an entry point without the interpreter's lock, as ctypes does: a launch into a full
 // queue waits for the device, which may itself wait for a host function of another thread.
+struct Unlocked {
+    PyThreadState *const thread = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(thread); }
+};
+
 template <typename Fn, typename... Args> int unlocked(Fn fn, Args... args)
 {
-    PyThreadState *const thread = PyEval_SaveThread();
-    const int rc = fn(args...);
-    PyEval_RestoreThread(thread);
-    return rc;
+    const Unlocked on;
+    return fn(args...);
 }
 
 // Runs `body` (Reader, entry point, stream argument) and turns what it throws into a
